@@ -73,6 +73,76 @@ int check_shape(int B, int H, int Nq, int Nk, int d, int block) {
 
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+#define SA_REQUIRE_I32(ptr)                                    \
+  SA_REQUIRE((ptr) != nullptr && ((uintptr_t)(ptr) & 3u) == 0, \
+             "%s must be a non-null 4-byte aligned pointer", #ptr)
+
+int check_row_strides(const sa::RowStrides& s, const char* name) {
+  SA_REQUIRE(s.b >= 0 && s.h >= 0 && s.t >= 0 && s.b % 8 == 0 && s.h % 8 == 0 && s.t % 8 == 0,
+             "the strides of %s must be non-negative multiples of 8 elements", name);
+  return SA_OK;
+}
+
+// Checks and packs the arguments that describe a paged cache; n == 0 (like B*H == 0) means
+// that the call does nothing and the buffers are not looked at.
+int paged_view(sa::PagedView* c, void* k, void* v, uint8_t* k_scale, uint8_t* v_scale, int dtype,
+               int num_pages, int page, const int32_t* page_table, int table_width,
+               int64_t table_stride, int B, int H, int d, int n, int32_t* err_flag) {
+  SA_REQUIRE(B >= 0 && H >= 0, "B and H must be >= 0");
+  SA_REQUIRE(d == 64 || d == 128, "d must be 64 or 128 (got %d)", d);
+  SA_REQUIRE((long long)B * H <= 65535, "B*H must be <= 65535 (got %lld)", (long long)B * H);
+  SA_REQUIRE(dtype == SA_CACHE_BF16 || dtype == SA_CACHE_E4M3, "cache_dtype must be BF16 or E4M3");
+  int log2 = 4;
+  while (log2 < 8 && (1 << log2) != page) ++log2;
+  SA_REQUIRE((1 << log2) == page, "page must be 16, 32, 64, 128 or 256 (got %d)", page);
+  SA_REQUIRE(num_pages >= 0 && table_width >= 0, "num_pages and table_width must be >= 0");
+  SA_REQUIRE((long long)table_width * page <= INT32_MAX, "table_width * page must be < 2^31");
+  SA_REQUIRE(B <= 1 || table_stride >= table_width,
+             "table_stride must be at least table_width (got %lld, %d)", (long long)table_stride,
+             table_width);
+  if (err_flag) SA_REQUIRE(((uintptr_t)err_flag & 3u) == 0, "err_flag must be 4-byte aligned");
+  if ((long long)B * H != 0 && n != 0) {
+    if (num_pages > 0) {
+      SA_REQUIRE(k != nullptr && aligned16(k) && v != nullptr && aligned16(v),
+                 "k_pages and v_pages must be non-null 16-byte aligned pointers");
+      SA_REQUIRE(k != v, "k_pages and v_pages must not be the same buffer");
+      if (dtype == SA_CACHE_E4M3)
+        SA_REQUIRE(k_scale != nullptr && aligned16(k_scale) && v_scale != nullptr &&
+                       aligned16(v_scale) && k_scale != v_scale,
+                   "an e4m3 cache needs k_scale and v_scale, 16-byte aligned and distinct");
+    }
+    if (table_width > 0) SA_REQUIRE_I32(page_table);
+  }
+  *c = sa::PagedView{k, v, k_scale, v_scale, dtype == SA_CACHE_E4M3, num_pages, log2, H, d,
+                     page_table, table_width, B <= 1 ? 0 : table_stride, err_flag};
+  return SA_OK;
+}
+
+int check_decode_shape(int B, int Hq, int Hkv, int T, int d) {
+  SA_REQUIRE(B >= 0 && Hq >= 0 && Hkv >= 0, "B, Hq and Hkv must be >= 0");
+  SA_REQUIRE(d == 64 || d == 128, "d must be 64 or 128 (got %d)", d);
+  SA_REQUIRE(T >= 1 && T <= SA_MAX_DECODE_TOKENS, "T must be in [1, %d] (got %d)",
+             SA_MAX_DECODE_TOKENS, T);
+  SA_REQUIRE(Hkv == 0 ? Hq == 0 : Hq % Hkv == 0, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+  SA_REQUIRE((long long)B * Hkv <= 65535, "B*Hkv must be <= 65535");
+  SA_REQUIRE((long long)B * Hq <= 1 << 30, "B*Hq must be <= 2^30");
+  return SA_OK;
+}
+
+int sm_count(int* sms) {
+  static int cache[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64 && cache[dev] > 0) {
+    *sms = cache[dev];
+    return SA_OK;
+  }
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(SA_ERR_LAUNCH, "SM count: %s", cudaGetErrorString(e));
+  if (dev >= 0 && dev < 64) cache[dev] = *sms;
+  return SA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -528,6 +598,109 @@ int sparse_attn_forward_split(const uint16_t* q, const uint16_t* k, const uint16
                     B, H, Nq, Nk, d, block, order, cdiv(Nq, block), nkb, scale, out, out_dtype,
                     err_flag, splits, work};
   return launched(sa::launch_forward(p, static_cast<cudaStream_t>(stream)), "forward launch");
+}
+
+int sparse_attn_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_sb, int64_t k_sh,
+                             int64_t k_st, int64_t v_sb, int64_t v_sh, int64_t v_st, int B, int H,
+                             int T, int d, const int32_t* page_table, int table_width,
+                             int64_t table_stride, const int32_t* start, const int32_t* count,
+                             void* k_pages, void* v_pages, uint8_t* k_scale, uint8_t* v_scale,
+                             int cache_dtype, int num_pages, int page, int32_t* err_flag,
+                             void* stream) {
+  SA_REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
+  sa::PagedView c;
+  if (int rc = paged_view(&c, k_pages, v_pages, k_scale, v_scale, cache_dtype, num_pages, page,
+                          page_table, table_width, table_stride, B, H, d, T, err_flag))
+    return rc;
+  SA_REQUIRE((long long)H * T <= INT32_MAX, "H*T must be < 2^31");
+  const sa::RowStrides ks{k_sb, k_sh, k_st}, vs{v_sb, v_sh, v_st};
+  if (int rc = check_row_strides(ks, "k")) return rc;
+  if (int rc = check_row_strides(vs, "v")) return rc;
+  if ((long long)B * H * T == 0) return ok();
+  SA_REQUIRE_PTR(k);
+  SA_REQUIRE_PTR(v);
+  SA_REQUIRE_I32(start);
+  if (count) SA_REQUIRE_I32(count);
+  if (int rc = check_device()) return rc;
+  sa::CacheAppendArgs p{c, k, v, ks, vs, B, T, start, count};
+  return launched(sa::launch_cache_append(p, static_cast<cudaStream_t>(stream)),
+                  "cache append launch");
+}
+
+int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                           const uint8_t* v_scale, int cache_dtype, int num_pages, int page,
+                           const int32_t* page_table, int table_width, int64_t table_stride,
+                           const int32_t* first, const int32_t* lens, int B, int H, int N, int d,
+                           uint16_t* k, uint16_t* v, int64_t k_sb, int64_t k_sh, int64_t k_st,
+                           int64_t v_sb, int64_t v_sh, int64_t v_st, int32_t* err_flag,
+                           void* stream) {
+  SA_REQUIRE(N >= 0, "N must be >= 0 (got %d)", N);
+  sa::PagedView c;
+  if (int rc = paged_view(&c, const_cast<void*>(k_pages), const_cast<void*>(v_pages),
+                          const_cast<uint8_t*>(k_scale), const_cast<uint8_t*>(v_scale),
+                          cache_dtype, num_pages, page, page_table, table_width, table_stride, B,
+                          H, d, N, err_flag))
+    return rc;
+  const sa::RowStrides ks{k_sb, k_sh, k_st}, vs{v_sb, v_sh, v_st};
+  if (int rc = check_row_strides(ks, "k")) return rc;
+  if (int rc = check_row_strides(vs, "v")) return rc;
+  if ((long long)B * H == 0 || N == 0) return ok();
+  SA_REQUIRE_PTR(k);
+  SA_REQUIRE_PTR(v);
+  SA_REQUIRE(k != v, "k and v must not be the same buffer");
+  SA_REQUIRE_I32(lens);
+  if (first) SA_REQUIRE_I32(first);
+  if (int rc = check_device()) return rc;
+  sa::CacheReadArgs p{c, k, v, ks, vs, B, N, first, lens};
+  return launched(sa::launch_cache_read(p, static_cast<cudaStream_t>(stream)), "cache read launch");
+}
+
+int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
+                       int Hkv, int T, int d, const void* k_pages, const void* v_pages,
+                       const uint8_t* k_scale, const uint8_t* v_scale, int cache_dtype,
+                       int num_pages, int page, const int32_t* page_table, int table_width,
+                       int64_t table_stride, const int32_t* lens, const int32_t* kv_idx,
+                       const int32_t* kv_cnt, int cap, float scale, void* work, void* out,
+                       int out_dtype, float* lse, int32_t* err_flag, void* stream) {
+  if (int rc = check_decode_shape(B, Hq, Hkv, T, d)) return rc;
+  sa::PagedView c;
+  if (int rc = paged_view(&c, const_cast<void*>(k_pages), const_cast<void*>(v_pages),
+                          const_cast<uint8_t*>(k_scale), const_cast<uint8_t*>(v_scale),
+                          cache_dtype, num_pages, page, page_table, table_width, table_stride, B,
+                          Hkv, d, Hq, err_flag))
+    return rc;
+  const sa::RowStrides qs{q_sb, q_sh, q_st};
+  if (int rc = check_row_strides(qs, "q")) return rc;
+  SA_REQUIRE(out_dtype == SA_OUT_F32 || out_dtype == SA_OUT_BF16, "out_dtype must be F32 or BF16");
+  SA_REQUIRE(std::isfinite(scale), "scale must be finite");
+  SA_REQUIRE((kv_idx != nullptr) == (kv_cnt != nullptr), "kv_idx and kv_cnt go together");
+  SA_REQUIRE(kv_idx == nullptr || cap >= 0, "cap must be >= 0");
+  if ((long long)B * Hq == 0) return ok();
+  SA_REQUIRE_PTR(q);
+  SA_REQUIRE_PTR(out);
+  SA_REQUIRE_I32(lens);
+  if (kv_idx) {
+    SA_REQUIRE_I32(kv_idx);
+    SA_REQUIRE_I32(kv_cnt);
+  }
+  if (lse) SA_REQUIRE(((uintptr_t)lse & 3u) == 0, "lse must be 4-byte aligned");
+  if (int rc = check_device()) return rc;
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  if (sa::decode_work_bytes(B, Hq, Hkv, T, d, sms)) SA_REQUIRE_PTR(work);
+  sa::DecodeArgs p{c, q, qs, B, Hq, T, lens, kv_idx, kv_cnt, cap, scale, sms, work, out, out_dtype,
+                   lse};
+  return launched(sa::launch_decode(p, static_cast<cudaStream_t>(stream)), "decode launch");
+}
+
+int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms, size_t* bytes) {
+  if (int rc = check_decode_shape(B, Hq, Hkv, T, d)) return rc;
+  SA_REQUIRE(bytes != nullptr, "bytes must be non-null");
+  SA_REQUIRE(sms >= 0, "sms must be >= 0");
+  if (sms == 0)
+    if (int rc = sm_count(&sms)) return rc;
+  *bytes = (long long)B * Hq == 0 ? 0 : sa::decode_work_bytes(B, Hq, Hkv, T, d, sms);
+  return ok();
 }
 
 }  // extern "C"

@@ -91,6 +91,59 @@ struct PermuteArgs {
   void* dst;
 };
 
+// A paged cache and the page tables of the sequences of one call.
+struct PagedView {
+  void *k, *v;                // [num_pages][H][page][d] bf16, or e4m3 codes
+  uint8_t *k_scale, *v_scale; // [num_pages][H][page] E8M0 (e4m3 only)
+  int e4m3, num_pages, page_log2, H, d;
+  const int32_t* table;       // [B] rows of table_width page numbers, table_stride apart
+  int table_width;
+  int64_t table_stride;
+  int32_t* err_flag;
+};
+constexpr int SA_FLAG_INDEX_BIT = 1 << 21;  // SA_FLAG_INDEX of the C header
+
+struct RowStrides {  // in elements, between batches, heads and tokens
+  int64_t b, h, t;
+};
+
+struct CacheAppendArgs {
+  PagedView c;
+  const uint16_t *k, *v;
+  RowStrides ks, vs;
+  int B, T;
+  const int32_t *start, *count;  // count may be null: T for every sequence
+};
+
+struct CacheReadArgs {
+  PagedView c;
+  uint16_t *k, *v;
+  RowStrides ks, vs;
+  int B, N;
+  const int32_t *first, *lens;  // first may be null: 0 for every sequence
+};
+
+struct DecodeArgs {
+  PagedView c;
+  const uint16_t* q;
+  RowStrides qs;
+  int B, Hq, T;
+  const int32_t* lens;
+  const int32_t *kv_idx, *kv_cnt;  // null: every page
+  int cap;
+  float scale;
+  int sms;
+  void* work;
+  void* out;
+  int out_dtype;
+  float* lse;  // may be null
+};
+
+cudaError_t launch_cache_append(const CacheAppendArgs& p, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheReadArgs& p, cudaStream_t st);
+cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st);
+size_t decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms);
+
 // Byte offsets of launch_kmeans's work buffers in cwork and iwork, and the two ends.
 struct KmeansLayout {
   size_t pieces, cnorm, part, cwork_end;

@@ -13,10 +13,14 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libsparse_attn.so")
 
-SA_OK, SA_ERR_INVALID, SA_ERR_LAUNCH, SA_ERR_TIMEOUT, SA_ERR_UNSUPPORTED, SA_ERR_RANGE = range(6)
+(SA_OK, SA_ERR_INVALID, SA_ERR_LAUNCH, SA_ERR_TIMEOUT, SA_ERR_UNSUPPORTED, SA_ERR_RANGE,
+ SA_ERR_INDEX) = range(7)
 SA_FLAG_RANGE = 1 << 20   # err_flag bit: a pooled fp16 table value did not fit
+SA_FLAG_INDEX = 1 << 21   # err_flag bit: a page number, length or position was out of range
 SA_ROUTE_TOPK, SA_ROUTE_MASS = 0, 1
 SA_OUT_F32, SA_OUT_BF16 = 0, 1
+SA_CACHE_BF16, SA_CACHE_E4M3 = 0, 1
+SA_MAX_DECODE_TOKENS = 16
 
 # Entry points declared in include/sparse_attn.h.
 EXPORTS = ("sparse_attn_table_sizes", "sparse_attn_pool", "sparse_attn_pool_incremental",
@@ -26,7 +30,8 @@ EXPORTS = ("sparse_attn_table_sizes", "sparse_attn_pool", "sparse_attn_pool_incr
            "sparse_attn_route_scores", "sparse_attn_kmeans_sizes", "sparse_attn_kmeans",
            "sparse_attn_permute_rows", "sparse_attn_kmeans_noalloc", "sparse_attn_wait_selftest",
            "sparse_attn_forward", "sparse_attn_forward_split", "sparse_attn_forward_work_bytes",
-           "sparse_attn_forward_split_plan", "sparse_attn_last_error")
+           "sparse_attn_forward_split_plan", "sparse_attn_cache_append", "sparse_attn_cache_read",
+           "sparse_attn_decode", "sparse_attn_decode_work_bytes", "sparse_attn_last_error")
 
 
 class SparseAttnError(RuntimeError):
@@ -39,6 +44,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_int64
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -71,6 +77,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sparse_attn_forward_work_bytes.argtypes = [_I] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.sparse_attn_forward_split_plan.argtypes = [_I] * 7 + [ctypes.POINTER(_I),
                                                               ctypes.POINTER(ctypes.c_size_t)]
+    lib.sparse_attn_cache_append.argtypes = [_P] * 2 + [_L] * 6 + [_I] * 4 + [_P, _I, _L] + \
+        [_P] * 6 + [_I] * 3 + [_P, _P]
+    lib.sparse_attn_cache_read.argtypes = [_P] * 4 + [_I] * 3 + [_P, _I, _L, _P, _P] + [_I] * 4 + \
+        [_P] * 2 + [_L] * 6 + [_P, _P]
+    lib.sparse_attn_decode.argtypes = [_P] + [_L] * 3 + [_I] * 5 + [_P] * 4 + [_I] * 3 + \
+        [_P, _I, _L] + [_P] * 3 + [_I, _F, _P, _P, _I, _P, _P, _P]
+    lib.sparse_attn_decode_work_bytes.argtypes = [_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
     for name in EXPORTS[:-1]:
         getattr(lib, name).restype = _I
     _lib = lib
@@ -232,6 +245,43 @@ def sparse_attn_forward_split_plan(B, H, Nq, Nk, d, block, sms=0):
     _check(load_library().sparse_attn_forward_split_plan(B, H, Nq, Nk, d, block, sms,
                                                          ctypes.byref(n), ctypes.byref(b)))
     return int(n.value), int(b.value)
+
+
+def sparse_attn_cache_append(k, v, k_strides, v_strides, B, H, T, d, page_table, table_width,
+                             table_stride, start, count, k_pages, v_pages, k_scale, v_scale,
+                             cache_dtype, num_pages, page, err_flag=None, stream=None):
+    """``k_strides``, ``v_strides``: elements between (batches, heads, tokens)."""
+    _check(load_library().sparse_attn_cache_append(
+        _ptr(k), _ptr(v), *k_strides, *v_strides, B, H, T, d, _ptr(page_table), table_width,
+        table_stride, _ptr(start), _ptr(count), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+        _ptr(v_scale), cache_dtype, num_pages, page, _ptr(err_flag), _stream(stream)))
+
+
+def sparse_attn_cache_read(k_pages, v_pages, k_scale, v_scale, cache_dtype, num_pages, page,
+                           page_table, table_width, table_stride, first, lens, B, H, N, d, k, v,
+                           k_strides, v_strides, err_flag=None, stream=None):
+    _check(load_library().sparse_attn_cache_read(
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), cache_dtype, num_pages, page,
+        _ptr(page_table), table_width, table_stride, _ptr(first), _ptr(lens), B, H, N, d, _ptr(k),
+        _ptr(v), *k_strides, *v_strides, _ptr(err_flag), _stream(stream)))
+
+
+def sparse_attn_decode(q, q_strides, B, Hq, Hkv, T, d, k_pages, v_pages, k_scale, v_scale,
+                       cache_dtype, num_pages, page, page_table, table_width, table_stride, lens,
+                       kv_idx, kv_cnt, cap, scale, work, out, out_dtype, lse=None, err_flag=None,
+                       stream=None):
+    _check(load_library().sparse_attn_decode(
+        _ptr(q), *q_strides, B, Hq, Hkv, T, d, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+        _ptr(v_scale), cache_dtype, num_pages, page, _ptr(page_table), table_width, table_stride,
+        _ptr(lens), _ptr(kv_idx), _ptr(kv_cnt), cap, scale, _ptr(work), _ptr(out), out_dtype,
+        _ptr(lse), _ptr(err_flag), _stream(stream)))
+
+
+def sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, sms=0) -> int:
+    """Scratch bytes of a decode on a device of ``sms`` SMs (0: the current device)."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, sms, ctypes.byref(out)))
+    return int(out.value)
 
 
 def sparse_attn_last_error() -> str:

@@ -51,7 +51,9 @@ enum {
   SA_ERR_LAUNCH = 2,       /* a CUDA launch or runtime call failed */
   SA_ERR_TIMEOUT = 3,      /* a bounded device wait gave up (reported through err_flag) */
   SA_ERR_UNSUPPORTED = 4,  /* the current device is not sm_100 */
-  SA_ERR_RANGE = 5         /* a pooled fp16 table value does not fit (reported through err_flag) */
+  SA_ERR_RANGE = 5,        /* a pooled fp16 table value does not fit (reported through err_flag) */
+  SA_ERR_INDEX = 6         /* a page number, length or position of a paged cache is out of range
+                              (reported through err_flag) */
 };
 
 /* Bit set in err_flag by the pool when a value of its fp16 outputs (V copy, value sums,
@@ -59,13 +61,20 @@ enum {
  * device waits that gave up (SA_ERR_TIMEOUT). */
 #define SA_FLAG_RANGE (1 << 20)
 
+/* Bit set in err_flag by the paged-cache entry points when a page number, a length or a
+ * position that they read from device memory lies outside the pool or the page table. The
+ * rows it stands for are then left out; nothing outside the caller's buffers is touched. */
+#define SA_FLAG_INDEX (1 << 21)
+
 enum { SA_ROUTE_TOPK = 0, SA_ROUTE_MASS = 1 };
 enum { SA_OUT_F32 = 0, SA_OUT_BF16 = 1 };
+enum { SA_CACHE_BF16 = 0, SA_CACHE_E4M3 = 1 };
 
 /* Largest number of KV blocks per head that routing and the forward accept. */
 #define SA_MAX_KV_BLOCKS 2048
 #define SA_MAX_CLUSTERS 4096
 #define SA_MAX_SPLITS 16
+#define SA_MAX_DECODE_TOKENS 16
 
 /*
  * Byte sizes of the pooled tables for a problem, written to sizes[0..6] in the
@@ -392,6 +401,93 @@ int sparse_attn_forward_work_bytes(int B, int H, int Nq, int d, int splits, size
  */
 int sparse_attn_forward_split_plan(int B, int H, int Nq, int Nk, int d, int block, int sms,
                                    int* splits, size_t* work_bytes);
+
+/*
+ * Paged key-value cache. A pool of num_pages pages of `page` tokens (16, 32, 64, 128 or
+ * 256) per kv head holds the K and V rows of every sequence; position p of sequence b
+ * lies in row p % page of pool page page_table[b][p / page]. The pages describe a
+ * contiguous growing cache; the paged layout, the 8-bit rows and the decode over them are
+ * this library's own, for serving many sequences beside the block-sparse call.
+ *   k_pages, v_pages  [num_pages,H,page,d]: bf16 (SA_CACHE_BF16) or e4m3 codes
+ *                     (SA_CACHE_E4M3)
+ *   k_scale, v_scale  [num_pages,H,page] E8M0 bytes, one per row: value = code *
+ *                     2^(byte - 127). Required for SA_CACHE_E4M3, ignored otherwise
+ *   page_table        [B] rows of table_width int32 page numbers, table_stride entries
+ *                     apart. Only the entries of positions in use are read; sequences may
+ *                     share pages that are only read
+ *   strides           *_sb, *_sh, *_st: elements between batches, heads and tokens of a
+ *                     tensor of bf16 rows of d contiguous values; multiples of 8 (16 bytes)
+ *   err_flag          optional device int32: SA_FLAG_INDEX is ORed into it when a page
+ *                     number of a position in use is outside [0, num_pages), a length is
+ *                     negative or past table_width * page (or past N for a read), a count
+ *                     is outside [0, T], a start or first row is negative, or an appended
+ *                     position is past table_width * page. Rows without a valid place are
+ *                     left out (not written, not attended). Sticky, like every err_flag.
+ * B * H <= 65535; B * Hq <= 2^30; pointers 16-byte aligned, int32 arrays and lse 4-byte
+ * aligned, scales 16-byte aligned. Nothing is allocated; one stream; graph capture is fine.
+ *
+ * sparse_attn_cache_append: token t < count[b] of sequence b (k, v [B,H,T,d] bf16) is
+ * written at position start[b] + t. For SA_CACHE_E4M3 each row is quantised as it is
+ * written: its scale is the smallest power of two s with max|x| / s <= 448 over the row's
+ * finite values (1 for a row of zeros, never below 2^-126), its codes are x / s rounded to
+ * nearest even; infinities and NaN become NaN. x / s is exact, so the only rounding is the
+ * one to e4m3 (at most 2^-4 of a value, or s * 2^-10). Two rows written to one place by one
+ * call (sequences sharing the page) leave either one there. One launch.
+ *   start   [B] int32; count [B] int32 or NULL (T for every sequence)
+ *
+ * sparse_attn_cache_read: rows first[b] <= t < lens[b] of sequence b are written to rows t
+ * of k, v [B,H,N,d] bf16 (a destination for sparse_attn_pool and sparse_attn_forward); all
+ * other rows are left as they were. An 8-bit row is code * 2^(byte - 127) rounded to bf16
+ * (exact down to bf16's subnormals). One launch.
+ *   first   [B] int32 or NULL (0); lens [B] int32, at most N
+ */
+int sparse_attn_cache_append(const uint16_t* k, const uint16_t* v, int64_t k_sb, int64_t k_sh,
+                             int64_t k_st, int64_t v_sb, int64_t v_sh, int64_t v_st, int B, int H,
+                             int T, int d, const int32_t* page_table, int table_width,
+                             int64_t table_stride, const int32_t* start, const int32_t* count,
+                             void* k_pages, void* v_pages, uint8_t* k_scale, uint8_t* v_scale,
+                             int cache_dtype, int num_pages, int page, int32_t* err_flag,
+                             void* stream);
+int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                           const uint8_t* v_scale, int cache_dtype, int num_pages, int page,
+                           const int32_t* page_table, int table_width, int64_t table_stride,
+                           const int32_t* first, const int32_t* lens, int B, int H, int N, int d,
+                           uint16_t* k, uint16_t* v, int64_t k_sb, int64_t k_sh, int64_t k_st,
+                           int64_t v_sb, int64_t v_sh, int64_t v_st, int32_t* err_flag,
+                           void* stream);
+
+/*
+ * Attention of the last T tokens of every sequence over its paged cache (T = 1: one new
+ * token). lens[b] counts the cached tokens, the T new ones (already appended) among them.
+ * Query head hq reads kv head hq / (Hq / Hkv); row t of sequence b attends the positions
+ * p < lens[b] - (T - 1 - t), of every page or of the listed ones:
+ *   l_p = scale * q . k_p,  o = sum_p e^(l_p) v_p / sum_p e^(l_p),  lse = ln sum_p e^(l_p)
+ * A row that attends nothing (an empty sequence, an empty list, t < T - lens[b]) gets
+ * o = 0 and lse = -inf. A position that a row does not attend never reaches it, whatever
+ * its K and V hold; an attended non-finite K or V gives a non-finite output.
+ *   q        [B,Hq,T,d] bf16 (strided), 1 <= T <= 16; Hq a multiple of Hkv
+ *   kv_idx   [B,Hkv,cap] int32 and kv_cnt [B,Hkv]: kept logical pages of each kv head in
+ *            the list format of routing (the lists of one query block, block = page;
+ *            distinct entries). Entries outside [0, table_width) are ignored; kv_cnt is
+ *            clamped to [0, cap]. Both NULL: every page
+ *   work     device scratch, 16-byte aligned, at least sparse_attn_decode_work_bytes(...)
+ *            bytes for the current device (may be NULL when that is 0). Its contents need
+ *            no initialisation; calls that may run at the same time need one each
+ *   out      [B,Hq,T,d] contiguous, fp32 or bf16;  lse [B,Hq,T] fp32 or NULL
+ * Logits, maxima, sums and accumulators are fp32. The result is the same bit for bit from
+ * run to run on one kind of device.
+ */
+int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
+                       int Hkv, int T, int d, const void* k_pages, const void* v_pages,
+                       const uint8_t* k_scale, const uint8_t* v_scale, int cache_dtype,
+                       int num_pages, int page, const int32_t* page_table, int table_width,
+                       int64_t table_stride, const int32_t* lens, const int32_t* kv_idx,
+                       const int32_t* kv_cnt, int cap, float scale, void* work, void* out,
+                       int out_dtype, float* lse, int32_t* err_flag, void* stream);
+
+/* Bytes of `work` that sparse_attn_decode needs on a device of `sms` SMs (0: the current
+ * device). They do not depend on the lengths or the table. Host only. */
+int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms, size_t* bytes);
 
 /* Message for the last error returned on the calling thread ("" if none). */
 const char* sparse_attn_last_error(void);
