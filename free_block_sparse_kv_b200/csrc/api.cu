@@ -96,7 +96,7 @@ int paged_view(sa::PagedView* c, void* k, void* v, uint8_t* k_scale, uint8_t* v_
   while (log2 < 8 && (1 << log2) != page) ++log2;
   SA_REQUIRE((1 << log2) == page, "page must be 16, 32, 64, 128 or 256 (got %d)", page);
   SA_REQUIRE(num_pages >= 0 && table_width >= 0, "num_pages and table_width must be >= 0");
-  SA_REQUIRE((long long)table_width * page <= INT32_MAX, "table_width * page must be < 2^31");
+  SA_REQUIRE((long long)table_width * page <= 1 << 30, "table_width * page must be <= 2^30");
   SA_REQUIRE(B <= 1 || table_stride >= table_width,
              "table_stride must be at least table_width (got %lld, %d)", (long long)table_stride,
              table_width);
@@ -125,7 +125,7 @@ int check_decode_shape(int B, int Hq, int Hkv, int T, int d) {
              SA_MAX_DECODE_TOKENS, T);
   SA_REQUIRE(Hkv == 0 ? Hq == 0 : Hq % Hkv == 0, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
   SA_REQUIRE((long long)B * Hkv <= 65535, "B*Hkv must be <= 65535");
-  SA_REQUIRE((long long)B * Hq <= 1 << 30, "B*Hq must be <= 2^30");
+  SA_REQUIRE((long long)B * Hq <= (1 << 30) / T, "B*Hq*T must be <= 2^30");
   return SA_OK;
 }
 
@@ -674,7 +674,8 @@ int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_
   SA_REQUIRE(out_dtype == SA_OUT_F32 || out_dtype == SA_OUT_BF16, "out_dtype must be F32 or BF16");
   SA_REQUIRE(std::isfinite(scale), "scale must be finite");
   SA_REQUIRE((kv_idx != nullptr) == (kv_cnt != nullptr), "kv_idx and kv_cnt go together");
-  SA_REQUIRE(kv_idx == nullptr || cap >= 0, "cap must be >= 0");
+  SA_REQUIRE(kv_idx == nullptr || (cap >= 0 && (long long)cap * page <= 1 << 30),
+             "cap must be >= 0 and cap * page <= 2^30");
   if ((long long)B * Hq == 0) return ok();
   SA_REQUIRE_PTR(q);
   SA_REQUIRE_PTR(out);

@@ -35,10 +35,10 @@ SA_DEVI int pool_page(const PagedView& c, int b, int lp) {
   return -1;
 }
 
-// Length of sequence b clamped to what its table row can hold.
+// Length of sequence b clamped to what its table row can hold (nothing without a pool).
 SA_DEVI int seq_len(const PagedView& c, const int32_t* lens, int b) {
   const int n = lens[b];
-  const int64_t most = (int64_t)c.table_width << c.page_log2;
+  const int64_t most = c.num_pages > 0 ? (int64_t)c.table_width << c.page_log2 : 0;
   if (n >= 0 && n <= most) return n;
   if (c.err_flag) atomicOr(c.err_flag, SA_FLAG_INDEX_BIT);
   return n < 0 ? 0 : (int)most;

@@ -423,7 +423,7 @@ int sparse_attn_forward_split_plan(int B, int H, int Nq, int Nk, int d, int bloc
  *                     is outside [0, T], a start or first row is negative, or an appended
  *                     position is past table_width * page. Rows without a valid place are
  *                     left out (not written, not attended). Sticky, like every err_flag.
- * B * H <= 65535; B * Hq <= 2^30; pointers 16-byte aligned, int32 arrays and lse 4-byte
+ * B * H <= 65535; B * Hq * T, table_width * page and cap * page <= 2^30; pointers 16-byte aligned, int32 arrays and lse 4-byte
  * aligned, scales 16-byte aligned. Nothing is allocated; one stream; graph capture is fine.
  *
  * sparse_attn_cache_append: token t < count[b] of sequence b (k, v [B,H,T,d] bf16) is

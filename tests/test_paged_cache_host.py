@@ -114,6 +114,7 @@ def test_refusals(lib):
         dict(q=None), dict(q=p + 8), dict(qs=(0, 0, 4)), dict(out=None), dict(out=p + 8),
         dict(odt=2), dict(lens=None), dict(lens=p + 2), dict(scale=float("inf")),
         dict(scale=float("nan")), dict(idx=p), dict(cnt=p), dict(idx=p, cnt=p, cap=-1),
+        dict(idx=p, cnt=p, cap=1 << 27),
         dict(idx=p + 2, cnt=p, cap=1), dict(idx=p, cnt=p + 2, cap=1), dict(lse=p + 2)]]
     for fn, kw in cases:
         with pytest.raises(C.SparseAttnError) as e:
