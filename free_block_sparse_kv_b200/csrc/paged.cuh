@@ -21,9 +21,9 @@ SA_DEVI float e8m0_value(uint32_t s) {
 
 // Two e4m3 codes (low 16 bits of v) -> two f16, exact.
 SA_DEVI uint32_t e4m3x2_to_f16x2(uint32_t v) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+  uint32_t y;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(y) : "h"(static_cast<uint16_t>(v)));
+  return y;
 }
 
 // Pool page of logical page `lp` of sequence b, or -1 (and SA_FLAG_INDEX) when the table
