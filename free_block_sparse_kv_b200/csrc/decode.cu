@@ -35,13 +35,9 @@
 namespace sa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kStages = 3;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBuckets = kThreads;     // scan entries kept in shared memory
+constexpr int kMaxWarps = 16;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 constexpr float kShift16 = 14.f;       // f16 weights are at most 2^14 (fp16 ends at 2^16)
-constexpr float kShift8 = 8.f;         // e4m3 weights are at most 2^8 (e4m3 ends at 448)
 
 // A segment: its sequence, kv head and first query row, its steps, and where it starts on the
 // line (which tells segments apart).
@@ -51,13 +47,28 @@ struct Place {
 };
 
 // What CTA c leaves for the joining kernel: the segment that starts in its share and runs
-// past it (at.b < 0: none), and how the line was cut.
+// past it (at.b < 0: none), and the last CTA that holds a part of it.
 struct Record {
   Place at;
-  long long total;
-  int ctas, pad[3];
+  int last, pad[5];
 };
 static_assert(sizeof(Record) == 48, "the partials behind the records start on 16 bytes");
+
+SA_DEVI long long div_floor(long long a, int b) {   // a >= 0, b > 0
+  return a < (1ll << 32) ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line cut into n shares that differ by one step at most.
+struct Cut {
+  long long q;
+  int r;
+  SA_DEVI Cut(long long total, int n) : q(n ? div_floor(total, n) : 0), r(n ? (int)(total - q * n) : 0) {}
+  SA_DEVI long long lo(int c) const { return q * c + min(c, r); }
+  SA_DEVI int share_of(long long x) const {   // x < total
+    const long long big = (q + 1) * r;
+    return (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+  }
+};
 
 // Rows of 64 bytes: two to a 128-byte line, so the XOR takes the row's second and third bit.
 template <int ROW>
@@ -93,40 +104,19 @@ SA_DEVI float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
 SA_DEVI void cp_async16_whole(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
 }
-SA_DEVI uint16_t e4m3x2(float lo, float hi) {
-  uint16_t y;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(y) : "f"(hi), "f"(lo));
-  return y;
-}
-SA_DEVI float2 e4m3x2_values(uint16_t v) {
-  const uint32_t h = e4m3x2_to_f16x2(v);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-// D = A(16x32 e4m3, row) * B(32x8 e4m3, col) + D, fp32 accumulate.
-SA_DEVI void mma_e4m3(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Two transposed 16x16 blocks of bytes: a lane gets, of column lane/4 (and lane/4 + 8), the
 // rows 4 (lane%4) .. + 3.
 SA_DEVI void ldsm_t8(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-// log2 of an E8M0 scale.
-SA_DEVI float e8m0_log2(uint32_t e) {
-  return e == 255u ? __uint_as_float(0x7FC00000u) : (float)e - 127.f;
-}
-
 // What a step's tiles are and where: shared-memory addresses of its K and V rows, scales
 // and tile positions, and the segment's length.
 struct Step {
   uint32_t k, v;
   const uint8_t* vp;      // V rows, generic
   const uint8_t* meta;
+  float2* sc;             // e4m3: (K scale, log2 of V scale) of every key, made by scales()
   int len, T;
   bool all;               // every key of the step is attended by every row
   SA_DEVI int pos(int t) const { return reinterpret_cast<const int*>(meta + 128)[t]; }
@@ -134,113 +124,189 @@ struct Step {
   SA_DEVI bool part(int t) const { return T > 1 && pos(t) < len && pos(t) + 16 > len - T + 1; }
 };
 
-template <int D, bool E4M3, bool PAIRED>
+// Rows are copied as they are stored, 16 bytes a lane, into swizzled rows.
+template <int D, bool E4M3, int WARPS, int STAGES>
 struct Layout {
   static constexpr bool kE4M3 = E4M3;
+  static constexpr int kWarps = WARPS, kStages = STAGES, kThreads = 32 * WARPS;
   static constexpr int kRow = D * (E4M3 ? 1 : 2);     // bytes of a cached row
   static constexpr int kKeys = 4096 / kRow;           // keys per step
   static constexpr int kSub = kKeys / 16;             // 16-key tiles per step
   static constexpr int kChunks = kRow / 16;
   static constexpr int kPad = D + 4;                  // floats between staged rows
   static constexpr int kMeta = 160;                   // scales (2 x kKeys), tile positions
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * (8192 + kMeta) + 256;
-  // Where key r of a 16-key tile lies: in order, or (PAIRED) the even keys, then the odd
-  // ones, so that rows i and i + 8 of a product's 16-row operand are neighbouring keys.
-  SA_DEVI static int place(int r) { return PAIRED ? (r & 1) * 8 + (r >> 1) : r; }
+  static constexpr int kScales = E4M3 ? kKeys * 8 : 0;
+  // Where key r of a 16-key tile lies, which is its row of the S^T tile. bf16: in order.
+  // e4m3: keys 4a, 4a+1 at 2a, 2a+1 and keys 4a+2, 4a+3 at 8+2a, 8+2a+1, the order in which
+  // a transposing load of bytes hands a lane four neighbouring keys of V.
+  SA_DEVI static int place(int r) {
+    return E4M3 ? (r >> 2) * 2 + (r & 1) + ((r >> 1) & 1) * 8 : r;
+  }
+  // Key of row r < 8 of the tile, and how far the key of row r + 8 is from it.
+  SA_DEVI static int key_of(int r) { return E4M3 ? (r >> 1) * 4 + (r & 1) : r; }
+  static constexpr int kKeyStep = E4M3 ? 2 : 8;
   // Shared-memory offset of the i-th 16-byte piece that a lane copies of a tile: the
-  // lane's own part and a compile-time part.
+  // lane's own part and a compile-time part (place() and the swizzle add up without carries).
   SA_DEVI static uint32_t lane_part(int lane) {
     const int r = lane / kChunks, c = lane % kChunks;
     return swz_row<kRow>(place(r), c);
   }
   SA_DEVI static uint32_t piece(uint32_t lane_off, int i) {
     constexpr int rows = 32 / kChunks;                // rows that one piece of a warp covers
-    const int r = place(i * rows);                    // (a multiple of 2: no carry into place)
+    const int r = place(i * rows);
     const int x = kRow == 64 ? (r >> 1) & 3 : r & 7;
     return (lane_off ^ (uint32_t)(x << 4)) + r * kRow;
   }
 };
 
-// A row of zeros is stored with scale 1. It adds nothing to the numerator, and must not set
-// the level that the other rows' weights are held at: its log2 scale becomes -inf. The four
-// lanes of a row group look at keys k0 and k1 of tile t.
+// The scales of a step's keys as values, a key to a lane. A row of zeros is stored with scale
+// 1; it adds nothing to the numerator, and must not set the level that the other rows'
+// weights are held at: its log2 scale becomes -inf.
 template <class L>
-SA_DEVI void zero_rows(const Step& w, int t, int lane, int k0, int k1, float (&vl)[2]) {
-  if (!__any_sync(~0u, vl[0] == 0.f || vl[1] == 0.f)) return;
+SA_DEVI void scales(const Step& w, int lane) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = t * 16 + L::place(i ? k1 : k0);
-    uint32_t any = 0;
-#pragma unroll
-    for (int c = 0; c < L::kChunks; c += 4) {
-      const uint4 y = *reinterpret_cast<const uint4*>(w.vp + swz_row<L::kRow>(row, c + (lane & 3)));
-      any |= (y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu;
+  for (int key = lane; key < L::kKeys; key += 32) {
+    const uint32_t kb = w.meta[key], vb = w.meta[L::kKeys + key];
+    float lv = __uint_as_float(0x4B000000u | vb) - 8388735.f;    // vb - 127
+    if (vb == 255u) lv = __uint_as_float(0x7FC00000u);
+    if (vb == 127u) {
+      const int row = (key & ~15) + L::place(key & 15);
+      uint32_t any = 0;
+#pragma unroll 1
+      for (int c = 0; c < L::kChunks; ++c) {
+        const uint4 y = *reinterpret_cast<const uint4*>(w.vp + swz_row<L::kRow>(row, c));
+        any |= (y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu;
+      }
+      if (any == 0) lv = -INFINITY;
     }
-    any |= __shfl_xor_sync(~0u, any, 1);
-    any |= __shfl_xor_sync(~0u, any, 2);
-    if (any == 0) vl[i] = -INFINITY;
+    w.sc[key] = make_float2(e8m0_value(kb), lv);
   }
+  __syncwarp();
 }
 
-// ---------------------------------------------------------------------------------------
-// 16-bit products: bf16 rows as they are, or (more than eight query rows) e4m3 codes as f16.
-// A lane owns the columns (query rows) 2q and 2q + 1 of each n-tile.
-// ---------------------------------------------------------------------------------------
-template <int D, bool E4M3, int NT>
-struct Math16 : Layout<D, E4M3, false> {
-  using L = Layout<D, E4M3, false>;
-  static constexpr int kRows = 8 * NT, kGroups = NT, kMt = D / 16;
-  uint32_t qf[NT][D / 16][2];
+// The arithmetic of a warp: 16-bit products of bf16 rows as they are, or of e4m3 codes as f16
+// (mma.sync has no 8-bit form on this architecture that is not these conversions done again
+// for every product). A lane owns the columns (query rows) 2q and 2q + 1 of each n-tile of
+// eight, and two keys of each 16-key tile. TWO: the weights take two 16-bit pieces.
+template <int D, bool E4M3, bool TWO, int NT, int WARPS, int STAGES>
+struct Math : Layout<D, E4M3, WARPS, STAGES> {
+  using L = Layout<D, E4M3, WARPS, STAGES>;
+  static constexpr int kRows = 8 * NT, kMt = D / 16;
+  // With 32 rows the queries would take 64 registers of a lane: they stay in shared memory.
+  static constexpr bool kQs = NT == 4;
+  static constexpr int kQueries = kQs ? kRows * D * 2 : 0;
+  // A warp's ring also takes its partial at the end of its share.
+  static constexpr int kSlotBytes = kRows * L::kPad * 4;
+  static constexpr int kRing = STAGES * 8192 > kSlotBytes ? STAGES * 8192 : (kSlotBytes + 255) / 256 * 256;
+  static constexpr size_t kSmem =
+      (size_t)WARPS * (kRing + STAGES * L::kMeta + L::kScales + kQueries) + 256;
+  uint32_t qf[kQs ? 1 : NT][D / 16][2];
+  uint32_t qs;                     // this warp's queries in shared memory (kQs)
+  int r0, len, R;
   float m[NT][2], l[NT][2], mv[NT][2], f[NT][2];
   int lim[NT][2];
   float o[kMt][NT][4];
   int lane, q4, r8;
 
-  SA_DEVI void begin(const DecodeArgs& p, int b, int h, int r0, int len) {
-    const int G = p.Hq / p.c.H, R = G * p.T;
+  SA_DEVI void fetch(const DecodeArgs& p, int b, int h, int nt, uint32_t (&x)[D / 16][2]) {
+    const int G = p.Hq / p.c.H;
+    const int r = r0 + nt * 8 + r8;
+    const int g = r / p.T, t = r - g * p.T;
+    const uint16_t* qp = p.q + b * p.qs.b + (int64_t)(h * G + g) * p.qs.h + t * p.qs.t;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + r8;
-      const int g = r / p.T, t = r - g * p.T;
-      const uint16_t* qp = p.q + b * p.qs.b + (int64_t)(h * G + g) * p.qs.h + t * p.qs.t;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[nt][ks][0] = qf[nt][ks][1] = 0;
-        if (r < R) {
-          if constexpr (E4M3) {   // the order in which a lane gets its K codes (see below)
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(qp + ks * 16 + 4 * q4));
-            qf[nt][ks][0] = y.x;
-            qf[nt][ks][1] = y.y;
-          } else {
-            qf[nt][ks][0] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * q4));
-            qf[nt][ks][1] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8 + 2 * q4));
-          }
+    for (int ks = 0; ks < D / 16; ++ks) {
+      x[ks][0] = x[ks][1] = 0;
+      if (r < R) {
+        if constexpr (E4M3) {   // the order in which a lane gets its K codes (see below)
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(qp + ks * 16 + 4 * q4));
+          x[ks][0] = y.x;
+          x[ks][1] = y.y;
+        } else {
+          x[ks][0] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * q4));
+          x[ks][1] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8 + 2 * q4));
         }
       }
-      float back = 1.f;
-      if constexpr (E4M3) {
-        uint32_t top = 0;
+    }
+  }
+  // bf16 queries of n-tile nt as operands, and the factor of each of the lane's columns.
+  SA_DEVI void finish(const DecodeArgs& p, int nt, uint32_t (&x)[D / 16][2]) {
+    float back = p.scale * kLog2e;
+    if constexpr (E4M3) {
+      uint32_t top = 0;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          top = __vmaxu2(top, __vmaxu2(qf[nt][ks][0] & 0x7FFF7FFFu, qf[nt][ks][1] & 0x7FFF7FFFu));
-        top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
-        top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
-        // exponent field of the row's largest value; 2^(141 - e) brings it to 2^14
-        const uint32_t e = max(max(top & 0xFFFFu, top >> 16) >> 7, 15u);
-        const float to = __uint_as_float((268u - e) << 23);
-        back = __uint_as_float((e - 14u) << 23);
+      for (int ks = 0; ks < D / 16; ++ks)
+        top = __vmaxu2(top, __vmaxu2(x[ks][0] & 0x7FFF7FFFu, x[ks][1] & 0x7FFF7FFFu));
+      top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
+      // exponent field of the row's largest value; 2^(141 - e) brings it to 2^14
+      const uint32_t e = max(max(top & 0xFFFFu, top >> 16) >> 7, 15u);
+      const float to = __uint_as_float((268u - e) << 23);
+      back *= __uint_as_float((e - 14u) << 23);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
+      for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qf[nt][ks][i] = pack_f16(bf16_lo(qf[nt][ks][i]) * to, bf16_hi(qf[nt][ks][i]) * to);
+        for (int i = 0; i < 2; ++i)
+          x[ks][i] = pack_f16(bf16_lo(x[ks][i]) * to, bf16_hi(x[ks][i]) * to);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[nt][i] = __shfl_sync(~0u, back, (2 * q4 + i) * 4);
+      const int rc = r0 + nt * 8 + 2 * q4 + i;
+      lim[nt][i] = len - (rc < R ? p.T - 1 - rc % p.T : 0);
+    }
+  }
+
+  // The segment's queries are asked for, and (start) made operands once they are there.
+  SA_DEVI void load(const DecodeArgs& p, int b, int h, int r0_, int len_) {
+    R = p.Hq / p.c.H * p.T;
+    r0 = r0_;
+    len = len_;
+    if constexpr (kQs) {
+#pragma unroll 1
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t x[D / 16][2];
+        fetch(p, b, h, nt, x);
+        store(nt, x);
       }
-      back *= p.scale * kLog2e;
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) fetch(p, b, h, nt, qf[nt]);
+    }
+  }
+  // n-tile nt's operands to or from rows of 2 D bytes: word q of a 16-column group is the
+  // first of the lane's pair, word 4 + q the second, so that a row-wise 8x8 load returns them.
+  SA_DEVI void store(int nt, const uint32_t (&x)[D / 16][2]) {
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(qs + swz(nt * 8 + r8, 2 * ks + i, 2 * D) + 4 * q4),
+                     "r"(x[ks][i]) : "memory");
+  }
+  SA_DEVI void start(const DecodeArgs& p) {
+    if constexpr (kQs) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t x[D / 16][2];
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)     // its own words: no other lane's store to wait for
+            asm volatile("ld.shared.b32 %0, [%1];\n"
+                         : "=r"(x[ks][i])
+                         : "r"(qs + swz(nt * 8 + r8, 2 * ks + i, 2 * D) + 4 * q4) : "memory");
+        finish(p, nt, x);
+        if (E4M3) store(nt, x);
+      }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) finish(p, nt, qf[nt]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        f[nt][i] = __shfl_sync(~0u, back, (2 * q4 + i) * 4);
-        const int rc = r0 + nt * 8 + 2 * q4 + i;
-        lim[nt][i] = len - (rc < R ? p.T - 1 - rc % p.T : 0);
         m[nt][i] = mv[nt][i] = -INFINITY;
         l[nt][i] = 0.f;
       }
@@ -254,12 +320,26 @@ struct Math16 : Layout<D, E4M3, false> {
   SA_DEVI static void mma(float* d, const uint32_t* a, const uint32_t* b) {
     if constexpr (E4M3) mma_f16(d, a, b[0], b[1]); else mma_bf16(d, a, b[0], b[1]);
   }
+  // The operands of 32 columns of n-tile nt: two per 16.
+  SA_DEVI void queries(int nt, int pair, uint32_t (&b)[2][2]) {
+    if constexpr (kQs) {
+      ldsm_x4(qs + swz(nt * 8 + (lane & 7), 4 * pair + (lane >> 3), 2 * D), b[0][0], b[0][1], b[1][0],
+              b[1][1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b[i][0] = qf[nt][2 * pair + i][0];
+        b[i][1] = qf[nt][2 * pair + i][1];
+      }
+    }
+  }
 
   SA_DEVI void compute(const Step& w) {
     constexpr int SUB = L::kSub;
+    if constexpr (E4M3) scales<L>(w, lane);
     float s[SUB][NT][4];
     float sv[E4M3 ? SUB : 1][NT][4];   // s + log2 of the key's V scale
-    const int mi = lane >> 3, mr = lane & 7;
+    const int mi = lane >> 3, mr = lane & 7, key = L::key_of(r8);
     const uint32_t ka = w.k + swz_row<L::kRow>(mr + (mi & 1) * 8, mi >> 1);
 #pragma unroll
     for (int t = 0; t < SUB; ++t) {
@@ -267,25 +347,34 @@ struct Math16 : Layout<D, E4M3, false> {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[t][nt][i] = 0.f;
-      // A = K: 16 keys x 16 values. For e4m3 a 16-byte chunk holds 16 values and a lane
-      // gets four neighbours, which stand for columns 2q, 2q+1, 2q+8, 2q+9 of the product;
-      // the query was loaded in the same order.
+      // A = K: 16 keys x 16 values, 32 values at a time. For e4m3 a 16-byte chunk holds 16
+      // values and a lane gets four neighbours, which stand for columns 2q, 2q+1, 2q+8 and
+      // 2q+9 of the product; the queries are in the same order.
 #pragma unroll
-      for (int x = 0; x < L::kChunks / 2; ++x) {
-        uint32_t a[4];
-        ldsm_x4((ka ^ (uint32_t)(2 * x << 4)) + t * 16 * L::kRow, a[0], a[1], a[2], a[3]);
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t a[2][4];
         if constexpr (E4M3) {
+          uint32_t y[4];
+          ldsm_x4((ka ^ (uint32_t)(2 * x << 4)) + t * 16 * L::kRow, y[0], y[1], y[2], y[3]);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t af[4] = {e4m3x2_to_f16x2(a[2 * y]), e4m3x2_to_f16x2(a[2 * y + 1]),
-                                    e4m3x2_to_f16x2(a[2 * y] >> 16),
-                                    e4m3x2_to_f16x2(a[2 * y + 1] >> 16)};
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(s[t][nt], af, qf[nt][2 * x + y]);
-          }
+            for (int j = 0; j < 2; ++j) {
+              a[i][j] = e4m3x2_to_f16x2(y[2 * i + j]);
+              a[i][2 + j] = e4m3x2_to_f16x2(y[2 * i + j] >> 16);
+            }
         } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(s[t][nt], a, qf[nt][x]);
+          for (int i = 0; i < 2; ++i)
+            ldsm_x4((ka ^ (uint32_t)(2 * (2 * x + i) << 4)) + t * 16 * L::kRow, a[i][0], a[i][1],
+                    a[i][2], a[i][3]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t b[2][2];
+          queries(nt, x, b);
+          mma(s[t][nt], a[0], b[0]);
+          mma(s[t][nt], a[1], b[1]);
         }
       }
       // scale to base 2 and mask
@@ -293,10 +382,10 @@ struct Math16 : Layout<D, E4M3, false> {
       if constexpr (E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          ks[i] = e8m0_value(w.meta[t * 16 + r8 + 8 * i]);
-          vl[i] = e8m0_log2(w.meta[L::kKeys + t * 16 + r8 + 8 * i]);
+          const float2 sc = w.sc[t * 16 + key + L::kKeyStep * i];
+          ks[i] = sc.x;
+          vl[i] = sc.y;
         }
-        zero_rows<L>(w, t, lane, r8, r8 + 8, vl);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -308,12 +397,12 @@ struct Math16 : Layout<D, E4M3, false> {
           if constexpr (E4M3) sv[t][nt][i] = x + vl[i >> 1];
         }
       if (!w.all) {
-        const int pos0 = w.pos(t);
+        const int pos0 = w.pos(t) + key;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (pos0 + r8 + 8 * (i >> 1) >= lim[nt][i & 1]) {
+            if (pos0 + L::kKeyStep * (i >> 1) >= lim[nt][i & 1]) {
               s[t][nt][i] = -INFINITY;
               if constexpr (E4M3) sv[t][nt][i] = -INFINITY;
             }
@@ -327,9 +416,10 @@ struct Math16 : Layout<D, E4M3, false> {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = s[0][nt][i], y = E4M3 ? sv[0][nt][i] : 0.f;
+        float x = fmaxf(s[0][nt][i], s[0][nt][i + 2]), y = 0.f;
+        if constexpr (E4M3) y = fmaxf(sv[0][nt][i], sv[0][nt][i + 2]);
 #pragma unroll
-        for (int t = 0; t < SUB; ++t) {
+        for (int t = 1; t < SUB; ++t) {
           x = fmaxf(x, fmaxf(s[t][nt][i], s[t][nt][i + 2]));
           if constexpr (E4M3) y = fmaxf(y, fmaxf(sv[t][nt][i], sv[t][nt][i + 2]));
         }
@@ -360,7 +450,9 @@ struct Math16 : Layout<D, E4M3, false> {
           }
         }
     }
-    const uint32_t va = w.v + swz_row<L::kRow>(mr + (mi >> 1) * 8, mi & 1);
+    // V's addresses: bf16 as 8x8 blocks (keys mi>>1, values mi&1), e4m3 as two 16x16 blocks
+    const uint32_t va = E4M3 ? w.v + swz_row<L::kRow>(L::place(lane & 15), lane >> 4)
+                             : w.v + swz_row<L::kRow>(mr + (mi >> 1) * 8, mi & 1);
 #pragma unroll
     for (int t = 0; t < SUB; ++t) {
       // B = P^T in two pieces, by transposing each 8x8 block of S^T
@@ -379,42 +471,47 @@ struct Math16 : Layout<D, E4M3, false> {
           }
           if constexpr (E4M3) {
             const uint32_t hi = pack_f16(e[0], e[1]);
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
             ph[nt][hf] = movmatrix(hi);
-            pl[nt][hf] = movmatrix(pack_f16(e[0] - b.x, e[1] - b.y));
+            if constexpr (TWO) {
+              const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              pl[nt][hf] = movmatrix(pack_f16(e[0] - b.x, e[1] - b.y));
+            }
           } else {
             const uint32_t hi = pack_bf16(e[0], e[1]);
             ph[nt][hf] = movmatrix(hi);
             pl[nt][hf] = movmatrix(pack_bf16(e[0] - bf16_lo(hi), e[1] - bf16_hi(hi)));
           }
         }
-      // A = V^T. For e4m3 the transposed load moves pairs of neighbouring values; even
-      // ones make one tile of 16 output columns and odd ones the next.
+      // A = V^T, 32 output columns at a time
       auto load_v = [&](int x, uint32_t (&a)[2][4]) {
-        uint32_t y[4];
-        ldsm_x4_t((va ^ (uint32_t)(2 * x << 4)) + t * 16 * L::kRow, y[0], y[1], y[2], y[3]);
+        if constexpr (E4M3) {
+          uint32_t y[4];
+          ldsm_t8((va ^ (uint32_t)(2 * x << 4)) + t * 16 * L::kRow, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (E4M3) {
-            a[0][i] = e4m3x2_to_f16x2(__byte_perm(y[i], 0, 0x4420));
-            a[1][i] = e4m3x2_to_f16x2(__byte_perm(y[i], 0, 0x4431));
-          } else {
-            a[0][i] = y[i];
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              a[i][j] = e4m3x2_to_f16x2(y[2 * i + j]);
+              a[i][2 + j] = e4m3x2_to_f16x2(y[2 * i + j] >> 16);
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            ldsm_x4_t((va ^ (uint32_t)(2 * (2 * x + i) << 4)) + t * 16 * L::kRow, a[i][0], a[i][1],
+                      a[i][2], a[i][3]);
         }
       };
-      constexpr int PER = E4M3 ? 2 : 1;    // output tiles of a load
       if (w.all || !w.part(t)) {
 #pragma unroll
-        for (int x = 0; x < L::kChunks / 2; ++x) {
+        for (int x = 0; x < D / 32; ++x) {
           uint32_t a[2][4];
           load_v(x, a);
 #pragma unroll
-          for (int y = 0; y < PER; ++y)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma(o[x * PER + y][nt], a[y], ph[nt]);
-              mma(o[x * PER + y][nt], a[y], pl[nt]);
+              mma(o[x * 2 + y][nt], a[y], ph[nt]);
+              if constexpr (TWO) mma(o[x * 2 + y][nt], a[y], pl[nt]);
             }
         }
       } else {
@@ -427,25 +524,25 @@ struct Math16 : Layout<D, E4M3, false> {
           uint32_t keep[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int k0 = w.pos(t) + 2 * q4 + 8 * i;
+            const int k0 = w.pos(t) + (E4M3 ? 4 * q4 + 2 * i : 2 * q4 + 8 * i);
             keep[i] = (k0 < mine ? 0xFFFFu : 0u) | (k0 + 1 < mine ? 0xFFFF0000u : 0u);
           }
 #pragma unroll
-          for (int x = 0; x < L::kChunks / 2; ++x) {
+          for (int x = 0; x < D / 32; ++x) {
             uint32_t a[2][4];
             load_v(x, a);
 #pragma unroll
-            for (int y = 0; y < PER; ++y) {
+            for (int y = 0; y < 2; ++y) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) a[y][i] &= keep[i >> 1];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
                 mma(z, a[y], ph[nt]);
-                mma(z, a[y], pl[nt]);
+                if constexpr (TWO) mma(z, a[y], pl[nt]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (lim[nt][i & 1] == mine) o[x * PER + y][nt][i] += z[i];
+                  if (lim[nt][i & 1] == mine) o[x * 2 + y][nt][i] += z[i];
               }
             }
           }
@@ -481,257 +578,15 @@ struct Math16 : Layout<D, E4M3, false> {
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = E4M3 ? 32 * (mt >> 1) + 2 * r8 + (mt & 1) + 16 * (i >> 1)
-                           : 16 * mt + r8 + 8 * (i >> 1);
-        to[(2 * q4 + (i & 1)) * L::kPad + c] = o[mt][g][i] * f[g][i & 1];
-      }
-  }
-};
-
-// ---------------------------------------------------------------------------------------
-// 8-bit products (up to eight query rows): the codes enter as they are, 32 to an instruction
-// at twice the rate and without a conversion; the other operand is split into e4m3 pieces,
-// each 2^-5 of the one before, that fill columns which few query rows would leave empty.
-// A query row takes two pieces: bf16's eight significant bits are two times four (what is
-// lost is below 2^-22 of the row's largest value). A weight takes four, 2^-16 of it. A tile
-// of eight columns is four query rows times two pieces; a lane owns one row of each such
-// quad, both its pieces, and the neighbouring keys 2i and 2i + 1 of a tile.
-// ---------------------------------------------------------------------------------------
-template <int D, int NQ>
-struct Math8 : Layout<D, true, true> {
-  using L = Layout<D, true, true>;
-  static constexpr int kRows = 4 * NQ, kGroups = 1, kCh = D / 16;
-  uint32_t qf[NQ][D / 32][2];
-  float m[NQ], l[NQ], mv[NQ], f[NQ];
-  int lim[NQ];
-  float o[kCh][NQ][2][4];
-  int lane, q4, r8;
-
-  SA_DEVI void begin(const DecodeArgs& p, int b, int h, int r0, int len) {
-    const int G = p.Hq / p.c.H, R = G * p.T;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int r = r0 + n * 4 + (r8 >> 1);
-      const int g = r / p.T, t = r - g * p.T;
-      const uint16_t* qp = p.q + b * p.qs.b + (int64_t)(h * G + g) * p.qs.h + t * p.qs.t;
-      uint2 x[D / 32][2];
-      uint32_t top = 0;
-#pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint2 y = make_uint2(0, 0);
-          if (r < R) y = __ldg(reinterpret_cast<const uint2*>(qp + ks * 32 + i * 16 + 4 * q4));
-          x[ks][i] = y;
-          top = __vmaxu2(top, __vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu));
-        }
-      top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
-      top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
-      // exponent field of the row's largest value; 2^(134 - e) brings it below 2^8
-      const uint32_t e = max(max(top & 0xFFFFu, top >> 16) >> 7, 8u);
-      const float to = __uint_as_float((261u - e) << 23);
-      const float back = __uint_as_float((e - 7u) << 23) * (p.scale * kLog2e);
-      auto codes = [&](uint32_t v) -> uint32_t {
-        v |= __vcmpgeu2(v & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;   // infinities as NaN
-        const float a = bf16_lo(v) * to, c = bf16_hi(v) * to;
-        const uint16_t y = e4m3x2(a, c);
-        const float2 z = e4m3x2_values(y);
-        return (r8 & 1) ? e4m3x2((a - z.x) * 32.f, (c - z.y) * 32.f) : y;
-      };
-#pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          qf[n][ks][i] = codes(x[ks][i].x) | (codes(x[ks][i].y) << 16);
-      f[n] = __shfl_sync(~0u, back, 8 * q4);
-      const int rc = r0 + n * 4 + q4;
-      lim[n] = len - (rc < R ? p.T - 1 - rc % p.T : 0);
-      m[n] = mv[n] = -INFINITY;
-      l[n] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[c][n][i >> 2][i & 3] = 0.f;
-    }
-  }
-
-  SA_DEVI void compute(const Step& w) {
-    constexpr int SUB = L::kSub;
-    float s[SUB][NQ][2], sv[SUB][NQ][2];    // keys 2i, 2i + 1 of a tile; sv: + log2 of V's scale
-    const int mi = lane >> 3, mr = lane & 7;
-    const uint32_t ka = w.k + swz_row<L::kRow>(mr + (mi & 1) * 8, mi >> 1);
-#pragma unroll
-    for (int t = 0; t < SUB; ++t) {
-      float c[NQ][4];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) {
-        uint32_t a[4];
-        ldsm_x4((ka ^ (uint32_t)(2 * ks << 4)) + t * 16 * L::kRow, a[0], a[1], a[2], a[3]);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_e4m3(c[n], a, qf[n][ks][0], qf[n][ks][1]);
-      }
-      const uint32_t kb = *reinterpret_cast<const uint16_t*>(w.meta + t * 16 + 2 * r8);
-      const uint32_t vb = *reinterpret_cast<const uint16_t*>(w.meta + L::kKeys + t * 16 + 2 * r8);
-      const float ks[2] = {e8m0_value(kb & 255u), e8m0_value(kb >> 8)};
-      float vl[2] = {e8m0_log2(vb & 255u), e8m0_log2(vb >> 8)};
-      zero_rows<L>(w, t, lane, 2 * r8, 2 * r8 + 1, vl);
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float x = fmaf(c[n][2 * i + 1], 1.f / 32.f, c[n][2 * i]) * (f[n] * ks[i]);
-          s[t][n][i] = x;
-          sv[t][n][i] = x + vl[i];
-        }
-      if (!w.all) {
-        const int pos0 = w.pos(t) + 2 * r8;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (pos0 + i >= lim[n]) s[t][n][i] = sv[t][n][i] = -INFINITY;
-      }
-    }
-    float nm[NQ], nv[NQ];
-    bool moved = false;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      nm[n] = s[0][n][0];
-      nv[n] = sv[0][n][0];
-#pragma unroll
-      for (int t = 0; t < SUB; ++t) {
-        nm[n] = fmaxf(nm[n], fmaxf(s[t][n][0], s[t][n][1]));
-        nv[n] = fmaxf(nv[n], fmaxf(sv[t][n][0], sv[t][n][1]));
-      }
-      moved |= nm[n] > m[n] || nv[n] > mv[n];
-    }
-    if (__any_sync(~0u, moved)) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        const float x = col_max(fmaxf(nm[n], m[n])), y = col_max(fmaxf(nv[n], mv[n]));
-        l[n] *= ex2a(m[n] - ref_of(x));
-        const float c = ex2a(mv[n] - ref_of(y));
-        m[n] = x;
-        mv[n] = y;
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[ch][n][i >> 2][i & 3] *= c;
-      }
-    }
-    const uint32_t va = w.v + (lane >> 4) * 16 * L::kRow + swz_row<L::kRow>(L::place(lane & 15), 0);
-#pragma unroll
-    for (int t = 0; t < SUB; t += 2) {
-      uint32_t pb[NQ][2][2];     // [quad][pieces 1, 2 | 3, 4][tile]
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        const float r = ref_of(m[n]), rv = ref_of(mv[n]) - kShift8;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          l[n] += ex2a(s[t + y][n][0] - r) + ex2a(s[t + y][n][1] - r);
-          float a = ex2a(sv[t + y][n][0] - rv), b = ex2a(sv[t + y][n][1] - rv);
-          uint32_t pc[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint16_t z = e4m3x2(a, b);
-            pc[j] = z;
-            if (j < 3) {
-              const float2 v = e4m3x2_values(z);
-              a = (a - v.x) * 32.f;
-              b = (b - v.y) * 32.f;
-            }
-          }
-          pb[n][0][y] = movmatrix(pc[0] | (pc[1] << 16));
-          pb[n][1][y] = movmatrix(pc[2] | (pc[3] << 16));
-        }
-      }
-      auto load_v = [&](int c, uint32_t* a) {
-        ldsm_t8((va ^ (uint32_t)(c << 4)) + t * 16 * L::kRow, a);
-      };
-      if (w.all || !(w.part(t) || w.part(t + 1))) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          uint32_t a[4];
-          load_v(c, a);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            mma_e4m3(o[c][n][0], a, pb[n][0][0], pb[n][0][1]);
-            mma_e4m3(o[c][n][1], a, pb[n][1][0], pb[n][1][1]);
-          }
-        }
-      } else {   // see the 16-bit products
-#pragma unroll 1
-        for (int tok = 0; tok < w.T; ++tok) {
-          const int mine = w.len - (w.T - 1 - tok);
-          uint32_t keep[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            keep[y] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (w.pos(t + y) + 4 * q4 + j < mine) keep[y] |= 0xFFu << (8 * j);
-          }
-#pragma unroll
-          for (int c = 0; c < kCh; ++c) {
-            uint32_t a[4];
-            load_v(c, a);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] &= keep[i >> 1];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_e4m3(z, a, pb[n][k][0], pb[n][k][1]);
-                if (lim[n] == mine)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[c][n][k][i] += z[i];
-              }
-          }
-        }
-      }
-    }
-  }
-
-  SA_DEVI void close(bool whole) {
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      l[n] = col_sum(l[n]);
-      float x = mv[n] == -INFINITY ? 0.f : ex2a(mv[n] - kShift8 - ref_of(m[n]));
-      if (whole) x = l[n] == 0.f ? 0.f : x / l[n];
-      f[n] = x;
-    }
-  }
-  template <class F>
-  SA_DEVI void stats(int, F fn) {
-    if (r8 == 0)
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) fn(n * 4 + q4, m[n], l[n]);
-  }
-  SA_DEVI void stage(int, float* to) {
-#pragma unroll
-    for (int c = 0; c < kCh; ++c)
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float* x = o[c][n][0] + 2 * i;
-          const float* y = o[c][n][1] + 2 * i;
-          to[(n * 4 + q4) * L::kPad + c * 16 + r8 + 8 * i] =
-              fmaf(fmaf(fmaf(y[1], 1.f / 32.f, y[0]), 1.f / 32.f, x[1]), 1.f / 32.f, x[0]) * f[n];
-        }
+      for (int i = 0; i < 4; ++i)
+        to[(2 * q4 + (i & 1)) * L::kPad + 16 * mt + r8 + 8 * (i >> 1)] = o[mt][g][i] * f[g][i & 1];
   }
 };
 
 // What the steps of one unit (a sequence, or with kept lists a sequence's kv head) look like.
 struct Unit {
   int len, n;                 // attended length, steps of each of its segments
-  long long keys;             // keys in list order
+  int keys;                   // keys in list order
 };
 
 template <class M>
@@ -740,8 +595,8 @@ SA_DEVI Unit unit_of(const DecodeArgs& p, int b, int h) {
   x.len = seq_len(p.c, p.lens, b);
   x.keys = x.len;
   if (p.kv_idx && x.len)
-    x.keys = (long long)min(max(p.kv_cnt[(int64_t)b * p.c.H + h], 0), p.cap) << p.c.page_log2;
-  x.n = (int)((x.keys + M::kKeys - 1) / M::kKeys);
+    x.keys = min(max(p.kv_cnt[(int64_t)b * p.c.H + h], 0), p.cap) << p.c.page_log2;
+  x.n = (x.keys + M::kKeys - 1) / M::kKeys;
   return x;
 }
 
@@ -784,11 +639,16 @@ SA_DEVI void put_lse(const DecodeArgs& p, int64_t row, float m, float l) {
 }
 
 template <int D, class M>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int units, int groups) {
+__global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, int units, int groups) {
+  constexpr int kWarps = M::kWarps, kStages = M::kStages, kThreads = M::kThreads;
+  constexpr int kBuckets = kThreads;     // scan entries kept in shared memory
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long s_prefix[kBuckets + 1], s_warp[kWarps];
-  __shared__ Place e_at[2 * kWarps];
+  __shared__ Place e_at[2 * kWarps];     // partials: of warp w, 2w at the head of its share, 2w + 1 at its end
+  __shared__ float s_ml[2 * kWarps][2][M::kRows], s_w[2 * kWarps][M::kRows];
+  __shared__ float s_max[2 * kWarps][M::kRows], s_sum[2 * kWarps][M::kRows];
   constexpr size_t kSlot = (size_t)M::kRows * (D + 2);   // floats of a global partial
+  asm volatile("griddepcontrol.launch_dependents;\n");   // the joining kernel may be set up
   uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int G = p.Hq / p.c.H, R = G * p.T;
@@ -800,8 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
   // ---- the line of steps: a scan over the units' weights
   const int per = (units + kBuckets - 1) / kBuckets;
   long long sum = 0;
-  for (int u = tid * per; u < min(units, (tid + 1) * per); ++u)
-    sum += (long long)unit_at(u).n * segs;
+  bool none = false;
+  for (int u = tid * per; u < min(units, (tid + 1) * per); ++u) {
+    const int n = unit_at(u).n;
+    sum += (long long)n * segs;
+    none |= n == 0;
+  }
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -819,10 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
   }
   s_prefix[tid] = before + incl - sum;
   if (tid == 0) s_prefix[kBuckets] = total;
-  __syncthreads();
 
   // rows of units without a key
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  const int empty = __syncthreads_or(none);
+  for (int u = blockIdx.x; empty && u < units; u += gridDim.x) {
     if (unit_at(u).n) continue;
     const int b = p.kv_idx ? u / p.c.H : u, h = p.kv_idx ? u - b * p.c.H : 0;
     const int64_t row0 = ((int64_t)b * p.Hq + h * G) * p.T;
@@ -836,16 +700,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
   const int ctas = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
   Record* rec = static_cast<Record*>(p.work) + blockIdx.x;
   const bool active = (int)blockIdx.x < ctas;
-  const long long lo_c = active ? blockIdx.x * total / ctas : 0;
-  const long long hi_c = active ? (blockIdx.x + 1) * total / ctas : 0;
-  const long long lo = lo_c + w * (hi_c - lo_c) / kWarps;
-  const int steps = (int)(lo_c + (w + 1) * (hi_c - lo_c) / kWarps - lo);
+  const Cut cut(total, ctas);
+  const long long lo_c = active ? cut.lo(blockIdx.x) : 0, hi_c = active ? cut.lo(blockIdx.x + 1) : 0;
+  const int n_c = (int)(hi_c - lo_c), n_q = n_c / kWarps, n_r = n_c % kWarps;
+  const long long lo = lo_c + n_q * w + min(w, n_r);
+  const int steps = n_q + (w < n_r);
   float* heads = reinterpret_cast<float*>(static_cast<Record*>(p.work) + gridDim.x);
   float* head = heads + ((size_t)blockIdx.x * kWarps + w) * kSlot;
   float* cta_slots = heads + (size_t)gridDim.x * kWarps * kSlot;
 
-  uint8_t* ring = smem + (size_t)w * kStages * 8192;
-  uint8_t* metas = smem + (size_t)kWarps * kStages * 8192 + (size_t)w * kStages * M::kMeta;
+  uint8_t* ring = smem + (size_t)w * M::kRing;
+  uint8_t* metas = smem + (size_t)kWarps * M::kRing + (size_t)w * kStages * M::kMeta;
+  float2* scale_values = reinterpret_cast<float2*>(smem + (size_t)kWarps * (M::kRing + kStages * M::kMeta) +
+                                                   (size_t)w * M::kScales);
 
   if (steps > 0) {
     Cursor cc;
@@ -863,92 +730,118 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
         cc.x = unit_at(++u);
       }
       const long long in = lo - at;
-      const int j = (int)(in / cc.x.n);
+      const int j = (int)div_floor(in, cc.x.n);
       cc.s = (int)(in - (long long)j * cc.x.n);
       cc.b = p.kv_idx ? u / p.c.H : u;
       cc.h = p.kv_idx ? u % p.c.H : j / groups;
       cc.r0 = (p.kv_idx ? j : j % groups) * M::kRows;
     }
-    Cursor ic = cc;
+    M mth;
+    mth.lane = lane;
+    mth.q4 = lane & 3;
+    mth.r8 = lane >> 2;
+    mth.qs = smem_u32(smem) + kWarps * (M::kRing + kStages * M::kMeta + M::kScales) + w * M::kQueries;
+    mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
 
-    // Page and first position of the 16-key tile `lane` of the issue cursor's step.
-    int pg = -1, pos = kNoPos;
-    auto look_up = [&]() {
-      pg = -1;
-      pos = kNoPos;
-      if (lane < M::kSub) {
-        const long long vi = (long long)ic.s * M::kKeys + lane * 16;
-        if (vi < ic.x.keys) {
-          int lp = (int)(vi >> p.c.page_log2);
-          if (p.kv_idx) lp = p.kv_idx[((int64_t)ic.b * p.c.H + ic.h) * p.cap + lp];
-          if ((unsigned)lp < (unsigned)p.c.table_width) {
-            const int at = (lp << p.c.page_log2) + ((int)vi & ((1 << p.c.page_log2) - 1));
-            if (at < ic.x.len) {
-              pg = pool_page(p.c, ic.b, lp);
-              if (pg >= 0) pos = at;
-            }
-          }
+    // Steps are looked up ahead of their copies, so that no copy waits for a table: while one
+    // step is copied, the page numbers of the next (n_*) and the list entries of the one
+    // after it (a cursor) are on their way. Lane t < kSub looks after 16-key tile t.
+    Cursor ac = cc;
+    const int in_page = (1 << p.c.page_log2) - 1;
+    int a_lp = 0, n_pos = kNoPos, n_pg = 0, n_h = 0, n_len = 0;
+    int to_list = steps, to_table = steps, to_issue = steps;
+    auto list = [&]() {        // logical page of the cursor's tile
+      if (--to_list < 0) return;
+      const int vi = ac.s * M::kKeys + lane * 16;
+      a_lp = -1;
+      if (lane < M::kSub && vi < ac.x.keys) {
+        a_lp = vi >> p.c.page_log2;
+        if (p.kv_idx) a_lp = p.kv_idx[((int64_t)ac.b * p.c.H + ac.h) * p.cap + a_lp];
+      }
+    };
+    auto table = [&]() {       // its page number and position; then on to the next step
+      if (--to_table < 0) return;
+      n_h = ac.h;
+      n_len = ac.x.len;
+      n_pos = kNoPos;
+      if ((unsigned)a_lp < (unsigned)p.c.table_width) {
+        const int at = (a_lp << p.c.page_log2) + ((ac.s * M::kKeys + lane * 16) & in_page);
+        if (at < n_len) {
+          n_pos = at;
+          n_pg = p.c.table[ac.b * p.c.table_stride + a_lp];
         }
       }
+      if (to_table > 0) next_step<M>(p, ac, R);
     };
     const uint32_t lane_off = M::lane_part(lane);
     const int lane_row = lane / M::kChunks;
-    int to_issue = steps;
+    const uint32_t page_bytes = (uint32_t)p.c.H * M::kRow << p.c.page_log2;   // < 2^32
+    const uint8_t* kbase = static_cast<const uint8_t*>(p.c.k) + lane * 16;
+    const uint8_t* vbase = static_cast<const uint8_t*>(p.c.v) + lane * 16;
     auto issue = [&](int st) {
-      if (to_issue > 0) {
+      if (--to_issue >= 0) {
         const uint32_t kdst = smem_u32(ring + st * 8192);
         uint8_t* meta = metas + st * M::kMeta;
-        if (lane < M::kSub) reinterpret_cast<int*>(meta + 128)[lane] = pos;
+        if (n_pos != kNoPos && (unsigned)n_pg >= (unsigned)p.c.num_pages) {
+          n_pos = kNoPos;
+          if (p.c.err_flag) atomicOr(p.c.err_flag, SA_FLAG_INDEX_BIT);
+        }
+        if (lane < M::kSub) reinterpret_cast<int*>(meta + 128)[lane] = n_pos;
+        const int pos0 = __shfl_sync(~0u, n_pos, 0), pg0 = __shfl_sync(~0u, n_pg, 0);
+        if (in_page + 1 >= M::kKeys && n_len - pos0 >= M::kKeys) {
+          // the whole step lies in one page
+          const uint32_t row = ((uint32_t)n_h << p.c.page_log2) + (pos0 & in_page);
+          const uint64_t at = (uint64_t)(uint32_t)pg0 * page_bytes + (uint64_t)row * M::kRow;
+          const uint8_t* ks = kbase + at;
+          const uint8_t* vs = vbase + at;
 #pragma unroll
-        for (int t = 0; t < M::kSub; ++t) {
-          const int tpg = __shfl_sync(~0u, pg, t), tpos = __shfl_sync(~0u, pos, t);
-          const int live = ic.x.len - tpos;      // rows of the tile that exist
-          int64_t row = 0;
-          if (tpg >= 0)
-            row = (((int64_t)tpg * p.c.H + ic.h) << p.c.page_log2) + (tpos & ((1 << p.c.page_log2) - 1));
-          const int64_t at = row * M::kRow + lane * 16;
-          const uint8_t* ks = static_cast<const uint8_t*>(p.c.k) + at;
-          const uint8_t* vs = static_cast<const uint8_t*>(p.c.v) + at;
-          if (live >= 16) {
-#pragma unroll
-            for (int i = 0; i < M::kChunks / 2; ++i) {
-              const uint32_t dst = kdst + t * 16 * M::kRow + M::piece(lane_off, i);
-              cp_async16_whole(dst, ks + i * 512);
-              cp_async16_whole(dst + 4096, vs + i * 512);
-            }
-          } else {
+          for (int i = 0; i < 8; ++i) {
+            constexpr int per_tile = M::kChunks / 2;
+            const uint32_t dst = kdst + i / per_tile * 16 * M::kRow + M::piece(lane_off, i % per_tile);
+            cp_async16_whole(dst, ks + i * 512);
+            cp_async16_whole(dst + 4096, vs + i * 512);
+          }
+          if constexpr (M::kE4M3) {
+            if (lane < 2 * M::kSub)
+              cp_async16_whole(smem_u32(meta) + lane * 16,
+                               (lane < M::kSub ? p.c.k_scale : p.c.v_scale - M::kKeys) +
+                                   at / M::kRow + lane * 16);
+          }
+        } else {
+#pragma unroll 1
+          for (int t = 0; t < M::kSub; ++t) {
+            const int pos = __shfl_sync(~0u, n_pos, t), pg = __shfl_sync(~0u, n_pg, t);
+            const int live = n_len - pos;     // rows of the tile that exist (< 0: no tile)
+            const uint32_t row = ((uint32_t)n_h << p.c.page_log2) + (pos & in_page);
+            const uint64_t at = live > 0 ? (uint64_t)(uint32_t)pg * page_bytes + (uint64_t)row * M::kRow : 0;
             // rows behind the last one are zeros here, whatever the page holds
 #pragma unroll
             for (int i = 0; i < M::kChunks / 2; ++i) {
               const uint32_t dst = kdst + t * 16 * M::kRow + M::piece(lane_off, i);
               const bool in = i * (32 / M::kChunks) + lane_row < live;
-              cp_async16(dst, in ? ks + i * 512 : static_cast<const uint8_t*>(p.c.k), in ? 16 : 0);
-              cp_async16(dst + 4096, in ? vs + i * 512 : static_cast<const uint8_t*>(p.c.v), in ? 16 : 0);
+              cp_async16(dst, in ? kbase + at + i * 512 : kbase, in ? 16 : 0);
+              cp_async16(dst + 4096, in ? vbase + at + i * 512 : vbase, in ? 16 : 0);
+            }
+            if constexpr (M::kE4M3) {
+              if (lane < 2 && live > 0)
+                cp_async16_whole(smem_u32(meta) + lane * M::kKeys + t * 16,
+                                 (lane ? p.c.v_scale : p.c.k_scale) + at / M::kRow);
             }
           }
-          if constexpr (M::kE4M3) {
-            if (lane < 2 && tpg >= 0)
-              cp_async16_whole(smem_u32(meta) + lane * M::kKeys + t * 16,
-                               (lane ? p.c.v_scale : p.c.k_scale) + row);
-          }
         }
-        if (--to_issue > 0) {
-          next_step<M>(p, ic, R);
-          look_up();
-        }
+        table();
+        list();
       }
       cp_async_commit();
     };
-    look_up();
+    list();
+    table();
+    list();
 #pragma unroll 1
     for (int st = 0; st < kStages; ++st) issue(st);
 
-    M mth;
-    mth.lane = lane;
-    mth.q4 = lane & 3;
-    mth.r8 = lane >> 2;
     long long seg0 = lo - cc.s;      // first step of the current segment
-    mth.begin(p, cc.b, cc.h, cc.r0, cc.x.len);
+    mth.start(p);
     int st = 0;
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
@@ -960,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
         sp.v = sp.k + 4096;
         sp.vp = ring + st * 8192 + 4096;
         sp.meta = metas + st * M::kMeta;
+        sp.sc = scale_values;
         sp.len = cc.x.len;
         sp.T = p.T;
         sp.all = true;
@@ -978,14 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
         __syncwarp();
         mth.close(whole);
 #pragma unroll
-        for (int g = 0; g < M::kGroups; ++g) {
+        for (int g = 0; g < M::kRows / 8; ++g) {
           mth.stats(g, [&](int r, float m, float l) {
             if (whole) {
               if (r < rows) put_lse(p, row0 + r, m, l);
             } else {
-              float* ml = last ? slot + M::kRows * M::kPad : head + M::kRows * D;
-              ml[r] = m;
-              ml[M::kRows + r] = l;
+              s_ml[2 * w + (last ? 1 : 0)][0][r] = m;
+              s_ml[2 * w + (last ? 1 : 0)][1][r] = l;
             }
           });
           float* buf = !whole && last ? slot + g * 8 * M::kPad
@@ -1010,7 +903,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
         issue(st);
         if (ends) {
           seg0 = lo + i + 1;
-          mth.begin(p, cc.b, cc.h, cc.r0, cc.x.len);
+          mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
+          mth.start(p);
         }
         st = st + 1 == kStages ? 0 : st + 1;
       }
@@ -1019,12 +913,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
   __syncthreads();
 
   // ---- join the partials of each segment that several warps of this CTA shared
-  if (tid == 0) *rec = Record{Place{-1, 0, 0, 0, 0}, total, ctas, {0, 0, 0}};
-  auto partial = [&](int e, int& stride) -> const float* {
-    stride = (e & 1) ? M::kPad : D;
-    return (e & 1) ? reinterpret_cast<const float*>(smem + (size_t)(e >> 1) * kStages * 8192)
-                   : heads + ((size_t)blockIdx.x * kWarps + (e >> 1)) * kSlot;
-  };
+  if (tid == 0) rec->at.b = -1;
+  // weights of the partials: entry e's row r against the largest maximum of its segment
+  for (int x = tid; x < 2 * kWarps * M::kRows; x += kThreads) {
+    const int e = x / M::kRows, r = x % M::kRows;
+    if (e_at[e].b < 0) continue;
+    const long long s0 = e_at[e].s0;
+    float mx = -INFINITY;
+    bool first = true;
+    for (int k = 0; k < 2 * kWarps; ++k)
+      if (e_at[k].b >= 0 && e_at[k].s0 == s0) {
+        mx = fmaxf(mx, s_ml[k][0][r]);
+        first &= k >= e;
+      }
+    s_w[e][r] = ex2a(s_ml[e][0][r] - ref_of(mx));
+    if (!first) continue;
+    float ls = 0.f;
+    for (int k = e; k < 2 * kWarps; ++k)
+      if (e_at[k].b >= 0 && e_at[k].s0 == s0) ls += ex2a(s_ml[k][0][r] - ref_of(mx)) * s_ml[k][1][r];
+    s_max[e][r] = mx;
+    s_sum[e][r] = ls;
+  }
+  __syncthreads();
   for (int e0 = 0; e0 < 2 * kWarps;) {
     const Place at = e_at[e0];
     if (at.b < 0) {
@@ -1033,70 +943,66 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p, int u
     }
     int e1 = e0 + 1;
     while (e1 < 2 * kWarps && (e_at[e1].b < 0 || e_at[e1].s0 == at.s0)) ++e1;
+    uint32_t mask = 0;         // the segment's partials
+    for (int e = e0; e < e1; ++e) mask |= (e_at[e].b >= 0 ? 1u : 0u) << e;
     const int rows = min(M::kRows, R - at.r0);
     const bool whole = at.s0 >= lo_c && at.s0 + at.n <= hi_c;
     const int64_t row0 = ((int64_t)at.b * p.Hq + at.h * G) * p.T + at.r0;
     float* dst = cta_slots + ((size_t)blockIdx.x * 2 + (at.s0 < lo_c ? 0 : 1)) * kSlot;
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), c = x % (D / 4) * 4;
-      float mx = -INFINITY;
-      for (int e = e0; e < e1; ++e) {
-        if (e_at[e].b < 0) continue;
-        int sd;
-        const float* s = partial(e, sd);
-        mx = fmaxf(mx, s[M::kRows * sd + r]);
-      }
-      float ls = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int e = e0; e < e1; ++e) {
-        if (e_at[e].b < 0) continue;
-        int sd;
-        const float* s = partial(e, sd);
-        const float a = ex2a(s[M::kRows * sd + r] - ref_of(mx));
-        const float4 v = *reinterpret_cast<const float4*>(s + r * sd + c);
-        ls += a * s[M::kRows * sd + M::kRows + r];
+#pragma unroll
+      for (int e = 0; e < 2 * kWarps; ++e) {
+        if (!(mask >> e & 1)) continue;
+        const float* s = (e & 1) ? reinterpret_cast<const float*>(smem + (size_t)(e >> 1) * M::kRing) + r * M::kPad
+                                 : heads + ((size_t)blockIdx.x * kWarps + (e >> 1)) * kSlot + r * D;
+        const float a = s_w[e][r];
+        const float4 v = *reinterpret_cast<const float4*>(s + c);
         y.x += a * v.x;
         y.y += a * v.y;
         y.z += a * v.z;
         y.w += a * v.w;
       }
+      const float ls = s_sum[e0][r];
       if (whole) {
         const float inv = ls == 0.f ? 0.f : 1.f / ls;
         put4(p, row0 + r, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-        if (c == 0) put_lse(p, row0 + r, mx, ls);
+        if (c == 0) put_lse(p, row0 + r, s_max[e0][r], ls);
       } else {
         *reinterpret_cast<float4*>(dst + r * D + c) = y;
         if (c == 0) {
-          dst[M::kRows * D + r] = mx;
+          dst[M::kRows * D + r] = s_max[e0][r];
           dst[M::kRows * D + M::kRows + r] = ls;
         }
       }
     }
-    if (!whole && at.s0 >= lo_c && tid == 0) rec->at = at;
+    if (!whole && at.s0 >= lo_c && tid == 0) {
+      rec->at = at;
+      rec->last = cut.share_of(at.s0 + at.n - 1);
+    }
     e0 = e1;
   }
 }
 
 // Joins the partials of the segment that starts in CTA blockIdx.x's share and spans CTAs:
 // one block per row, its groups of D/4 threads take every eighth (or sixteenth) partial.
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs p, int ctas_max) {
   constexpr int LN = D / 4, GRP = 256 / LN;
   __shared__ float red[8];
   __shared__ float4 acc[256];
   __shared__ float accl[GRP];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the main kernel's partials are there
   const Record rec = static_cast<const Record*>(p.work)[blockIdx.x];
   if (rec.at.b < 0) return;
   const int G = p.Hq / p.c.H, R = G * p.T, row = blockIdx.y, tid = threadIdx.x;
   if (row >= R - rec.at.r0) return;
   constexpr size_t kSlot = (size_t)ROWS * (D + 2);
   const float* slots = reinterpret_cast<const float*>(static_cast<const Record*>(p.work) + ctas_max) +
-                       (size_t)ctas_max * kWarps * kSlot;
+                       (size_t)ctas_max * WARPS * kSlot;
   // CTAs of the segment: blockIdx.x (slot 1), then those whose share starts inside it (slot 0)
-  const long long end = rec.at.s0 + rec.at.n;
-  int last = blockIdx.x + 1;
-  while (last < rec.ctas && last * rec.total / rec.ctas < end) ++last;
-  const int parts = last - blockIdx.x;
+  const int parts = rec.last - blockIdx.x + 1;
   auto slot = [&](int i) {
     return slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
   };
@@ -1150,7 +1056,7 @@ cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
   const long long most = (long long)p.B * p.c.H * groups *
                          (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) /
                               M::kKeys + 1);
-  const int ctas = (int)std::min<long long>(p.sms, (most + kWarps - 1) / kWarps);
+  const int ctas = (int)std::min<long long>(p.sms, (most + M::kWarps - 1) / M::kWarps);
   auto* kern = decode_kernel<D, M>;
   static std::atomic<bool> ready[64];   // per device: the shared-memory limit is raised
   int dev = 0;
@@ -1161,28 +1067,31 @@ cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
   }
-  kern<<<ctas, kThreads, M::kSmem, st>>>(p, units, groups);
+  kern<<<ctas, M::kThreads, M::kSmem, st>>>(p, units, groups);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = (int)std::min<long long>(R, M::kRows);
-  decode_join_kernel<D, M::kRows><<<dim3(ctas, rows), 256, 0, st>>>(p, ctas);
-  return cudaGetLastError();
+  // set up while the main kernel runs; it waits for that kernel's end before it reads
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, rows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, M::kRows, M::kWarps>, p, ctas);
 }
 
 // The fewest rows per segment that hold the R rows of a kv head, up to 32 (more take further
 // segments, which read the keys again).
-template <int D>
+template <int D, bool E4M3, bool TWO>
 cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st) {
   const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  if (p.c.e4m3) {
-    if (R <= 4) return run<D, Math8<D, 1>>(p, st);
-    if (R <= 8) return run<D, Math8<D, 2>>(p, st);
-    if (R <= 16) return run<D, Math16<D, true, 2>>(p, st);
-    return run<D, Math16<D, true, 4>>(p, st);
-  }
-  if (R <= 8) return run<D, Math16<D, false, 1>>(p, st);
-  if (R <= 16) return run<D, Math16<D, false, 2>>(p, st);
-  return run<D, Math16<D, false, 4>>(p, st);
+  if (R <= 8) return run<D, Math<D, E4M3, TWO, 1, 8, 3>>(p, st);
+  if (R <= 16) return run<D, Math<D, E4M3, TWO, 2, 8, 3>>(p, st);
+  return run<D, Math<D, E4M3, TWO, 4, 8, 2>>(p, st);
 }
 
 }  // namespace
@@ -1191,11 +1100,18 @@ size_t decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms) {
   if (B == 0 || Hq == 0) return 0;
   const long long R = (long long)(Hq / Hkv) * T;
   const int rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
-  return (size_t)sms * (sizeof(Record) + (kWarps + 2) * (size_t)rows * (d + 2) * 4);
+  return (size_t)sms * (sizeof(Record) + (kMaxWarps + 2) * (size_t)rows * (d + 2) * 4);
 }
 
 cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
-  return p.c.d == 64 ? run_rows<64>(p, st) : run_rows<128>(p, st);
+  const bool two = !p.c.e4m3 || p.out_dtype == SA_OUT_F32;
+  if (p.c.d == 64)
+    return !p.c.e4m3 ? run_rows<64, false, true>(p, st)
+           : two     ? run_rows<64, true, true>(p, st)
+                     : run_rows<64, true, false>(p, st);
+  return !p.c.e4m3 ? run_rows<128, false, true>(p, st)
+         : two     ? run_rows<128, true, true>(p, st)
+                   : run_rows<128, true, false>(p, st);
 }
 
 }  // namespace sa

@@ -15,7 +15,7 @@ namespace sa {
 
 // 2^(s - 127); 255 is NaN, 0 is 2^-127 (a subnormal fp32).
 SA_DEVI float e8m0_value(uint32_t s) {
-  const uint32_t bits = s == 0 ? 0x00400000u : (s == 255u ? 0x7FC00000u : s << 23);
+  const uint32_t bits = (s << 23) | (((s + 1u) & 255u) < 2u ? 0x00400000u : 0u);
   return __uint_as_float(bits);
 }
 
