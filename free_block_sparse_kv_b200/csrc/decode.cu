@@ -36,6 +36,10 @@ namespace sa {
 namespace {
 
 constexpr int kMaxWarps = 16;
+constexpr int kLaneUnits = 8;
+// A cluster per segment saves the scan, the partials' way through memory and the second
+// kernel, about as long as this many steps of a warp take.
+constexpr long long kClusterSlack = 4;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 constexpr float kShift16 = 14.f;       // f16 weights are at most 2^14 (fp16 ends at 2^16)
 
@@ -606,9 +610,11 @@ struct Cursor {
   Unit x;
 };
 
+// On by k steps of the segment, and to the next segment with a key from its end.
 template <class M>
-SA_DEVI void next_step(const DecodeArgs& p, Cursor& c, int R) {
-  if (++c.s < c.x.n) return;
+SA_DEVI void advance(const DecodeArgs& p, Cursor& c, int k, int R) {
+  c.s += k;
+  if (c.s < c.x.n) return;
   c.s = 0;
   c.r0 += M::kRows;
   if (c.r0 < R) return;
@@ -638,73 +644,137 @@ SA_DEVI void put_lse(const DecodeArgs& p, int64_t row, float m, float l) {
   if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, class M>
+// Zeros and lse -inf for n rows from row0 on.
+template <int D>
+SA_DEVI void put_empty(const DecodeArgs& p, int64_t row0, int64_t n, int tid, int threads) {
+  for (int64_t i = tid; i < n * (D / 4); i += threads)
+    put4(p, row0 + i / (D / 4), D, (int)(i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+  for (int64_t i = tid; i < n; i += threads) put_lse(p, row0 + i, 0.f, 0.f);
+}
+
+SA_DEVI uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+SA_DEVI void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+SA_DEVI uint32_t peer_addr(const void* p, int rank) {   // the same shared variable of another CTA
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+SA_DEVI float peer_f32(uint32_t a) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+SA_DEVI float4 peer_f32x4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+  return x;
+}
+
+// CLUSTER: cluster c of the grid takes segment c alone, its CTAs and their warps equal parts
+// of the steps, and joins the partials over distributed shared memory: one launch, no scan
+// of the lengths. Otherwise the line of all steps is cut as described at the top.
+template <int D, class M, bool CLUSTER>
 __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, int units, int groups) {
   constexpr int kWarps = M::kWarps, kStages = M::kStages, kThreads = M::kThreads;
   constexpr int kBuckets = kThreads;     // scan entries kept in shared memory
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long s_prefix[kBuckets + 1], s_warp[kWarps];
-  __shared__ Place e_at[2 * kWarps];     // partials: of warp w, 2w at the head of its share, 2w + 1 at its end
-  __shared__ float s_ml[2 * kWarps][2][M::kRows], s_w[2 * kWarps][M::kRows];
-  __shared__ float s_max[2 * kWarps][M::kRows], s_sum[2 * kWarps][M::kRows];
+  __shared__ long long s_prefix[CLUSTER ? 1 : kBuckets + 1], s_warp[kWarps];
+  // partials: of warp w, 2w at the head of its share, 2w + 1 at its end
+  __shared__ Place e_at[2 * kWarps];
+  __shared__ float s_ml[2 * kWarps][2][M::kRows];
+  __shared__ __align__(16) float s_cta[CLUSTER ? M::kRows * (D + 2) : 4];
   constexpr size_t kSlot = (size_t)M::kRows * (D + 2);   // floats of a global partial
-  asm volatile("griddepcontrol.launch_dependents;\n");   // the joining kernel may be set up
   uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int G = p.Hq / p.c.H, R = G * p.T;
   const int segs = (p.kv_idx ? 1 : p.c.H) * groups;   // segments of a unit
-  auto unit_at = [&](int u) {
-    return p.kv_idx ? unit_of<M>(p, u / p.c.H, u % p.c.H) : unit_of<M>(p, u, 0);
-  };
 
-  // ---- the line of steps: a scan over the units' weights
-  const int per = (units + kBuckets - 1) / kBuckets;
-  long long sum = 0;
-  bool none = false;
-  for (int u = tid * per; u < min(units, (tid + 1) * per); ++u) {
-    const int n = unit_at(u).n;
-    sum += (long long)n * segs;
-    none |= n == 0;
-  }
-  long long incl = sum;
+  long long lo_c, hi_c, total = 0;      // this CTA's steps
+  Cursor cc;                            // and (below) the warp's first one
+  int ctas = 0, per = 1;
+  bool by_warp = true;
+  long long incl = 0, mine = 0;         // steps up to and of this lane's (thread's) units
+  if (lane < 2) e_at[2 * w + lane].b = -1;
+  if constexpr (CLUSTER) {
+    const int size = units;              // CTAs of a cluster
+    const int seg = blockIdx.x / size, rank = blockIdx.x - seg * size;
+    const int bh = groups > 1 ? seg / groups : seg;
+    cc.b = bh / p.c.H;
+    cc.h = bh - cc.b * p.c.H;
+    cc.r0 = (seg - bh * groups) * M::kRows;
+    cc.x = unit_of<M>(p, cc.b, cc.h);
+    if (cc.x.n == 0) {                   // the whole cluster leaves
+      if (rank == 0)
+        put_empty<D>(p, ((int64_t)cc.b * p.Hq + cc.h * G) * p.T + cc.r0, min(M::kRows, R - cc.r0), tid,
+                     kThreads);
+      return;
+    }
+    const Cut cut(cc.x.n, size);
+    lo_c = cut.lo(rank);
+    hi_c = cut.lo(rank + 1);
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;\n");   // the joining kernel may be set up
+    // ---- the line of steps: a scan over the units' weights
+    auto unit_at = [&](int u) {
+      return p.kv_idx ? unit_of<M>(p, u / p.c.H, u % p.c.H) : unit_of<M>(p, u, 0);
+    };
+    // (up to 32 kLaneUnits units every warp scans them by itself, a run of them to a lane)
+    by_warp = units <= 32 * kLaneUnits;
+    per = by_warp ? (units + 31) / 32 : (units + kBuckets - 1) / kBuckets;
+    const int first = (by_warp ? lane : tid) * per;
+    bool none = false;
+    for (int u = first; u < min(units, first + per); ++u) {
+      const int n = unit_at(u).n;
+      incl += (long long)n * segs;
+      none |= n == 0;
+    }
+    mine = incl;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_warp[w] = incl;
-  if (tid < 2 * kWarps) e_at[tid].b = -1;
-  __syncthreads();
-  long long before = 0, total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += y;
+    }
+    bool empty;
+    if (by_warp) {
+      total = __shfl_sync(~0u, incl, 31);
+      empty = __any_sync(~0u, none);
+    } else {
+      if (lane == 31) s_warp[w] = incl;
+      __syncthreads();
+      long long before = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) before += s_warp[i];
-    total += s_warp[i];
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < w) before += s_warp[i];
+        total += s_warp[i];
+      }
+      s_prefix[tid] = before + incl - mine;
+      if (tid == 0) s_prefix[kBuckets] = total;
+      empty = __syncthreads_or(none);
+    }
+    // rows of units without a key
+    for (int u = blockIdx.x; empty && u < units; u += gridDim.x) {
+      if (unit_at(u).n) continue;
+      const int b = p.kv_idx ? u / p.c.H : u, h = p.kv_idx ? u - b * p.c.H : 0;
+      put_empty<D>(p, ((int64_t)b * p.Hq + h * G) * p.T, p.kv_idx ? R : (int64_t)p.Hq * p.T, tid, kThreads);
+    }
+    ctas = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
+    const Cut cut(total, ctas);
+    const bool active = (int)blockIdx.x < ctas;
+    lo_c = active ? cut.lo(blockIdx.x) : 0;
+    hi_c = active ? cut.lo(blockIdx.x + 1) : 0;
   }
-  s_prefix[tid] = before + incl - sum;
-  if (tid == 0) s_prefix[kBuckets] = total;
-
-  // rows of units without a key
-  const int empty = __syncthreads_or(none);
-  for (int u = blockIdx.x; empty && u < units; u += gridDim.x) {
-    if (unit_at(u).n) continue;
-    const int b = p.kv_idx ? u / p.c.H : u, h = p.kv_idx ? u - b * p.c.H : 0;
-    const int64_t row0 = ((int64_t)b * p.Hq + h * G) * p.T;
-    const int64_t rows = p.kv_idx ? R : (int64_t)p.Hq * p.T;
-    for (int64_t i = tid; i < rows * (D / 4); i += kThreads)
-      put4(p, row0 + i / (D / 4), D, (int)(i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-    for (int64_t i = tid; i < rows; i += kThreads) put_lse(p, row0 + i, 0.f, 0.f);
-  }
-
-  // ---- this CTA's and this warp's share
-  const int ctas = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
-  Record* rec = static_cast<Record*>(p.work) + blockIdx.x;
-  const bool active = (int)blockIdx.x < ctas;
-  const Cut cut(total, ctas);
-  const long long lo_c = active ? cut.lo(blockIdx.x) : 0, hi_c = active ? cut.lo(blockIdx.x + 1) : 0;
+  // ---- this warp's share
   const int n_c = (int)(hi_c - lo_c), n_q = n_c / kWarps, n_r = n_c % kWarps;
   const long long lo = lo_c + n_q * w + min(w, n_r);
   const int steps = n_q + (w < n_r);
+  Record* rec = static_cast<Record*>(p.work) + blockIdx.x;
   float* heads = reinterpret_cast<float*>(static_cast<Record*>(p.work) + gridDim.x);
   float* head = heads + ((size_t)blockIdx.x * kWarps + w) * kSlot;
   float* cta_slots = heads + (size_t)gridDim.x * kWarps * kSlot;
@@ -715,63 +785,67 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
                                                    (size_t)w * M::kScales);
 
   if (steps > 0) {
-    Cursor cc;
-    {
-      int a = 0, z = kBuckets;   // the last bucket that starts at or before lo
-      while (z - a > 1) {
-        const int mid = (a + z) / 2;
-        if (s_prefix[mid] <= lo) a = mid; else z = mid;
+    if constexpr (CLUSTER) {
+      cc.s = (int)lo;
+    } else {
+      int a = 0;                         // the last run of units that starts at or before lo
+      long long at;
+      if (by_warp) {
+        a = 31 - __clz(__ballot_sync(~0u, incl - mine <= lo && mine > 0));
+        at = __shfl_sync(~0u, incl - mine, a);
+      } else {
+        for (int z = kBuckets; z - a > 1;) {
+          const int mid = (a + z) / 2;
+          if (s_prefix[mid] <= lo) a = mid; else z = mid;
+        }
+        at = s_prefix[a];
       }
-      long long at = s_prefix[a];
       int u = a * per;
-      cc.x = unit_at(u);
-      while (at + (long long)cc.x.n * segs <= lo && u + 1 < units) {
-        at += (long long)cc.x.n * segs;
-        cc.x = unit_at(++u);
+      while (true) {
+        cc.b = p.kv_idx ? u / p.c.H : u;
+        cc.h = p.kv_idx ? u - cc.b * p.c.H : 0;
+        cc.x = unit_of<M>(p, cc.b, cc.h);
+        const long long n = (long long)cc.x.n * segs;
+        if (at + n > lo || u + 1 >= units) break;
+        at += n;
+        ++u;
       }
       const long long in = lo - at;
-      const int j = (int)div_floor(in, cc.x.n);
+      const int j = segs > 1 ? (int)div_floor(in, cc.x.n) : 0;
       cc.s = (int)(in - (long long)j * cc.x.n);
-      cc.b = p.kv_idx ? u / p.c.H : u;
-      cc.h = p.kv_idx ? u % p.c.H : j / groups;
-      cc.r0 = (p.kv_idx ? j : j % groups) * M::kRows;
+      if (!p.kv_idx) cc.h = groups > 1 ? j / groups : j;
+      cc.r0 = (p.kv_idx ? j : j - cc.h * groups) * M::kRows;
     }
     M mth;
     mth.lane = lane;
     mth.q4 = lane & 3;
     mth.r8 = lane >> 2;
     mth.qs = smem_u32(smem) + kWarps * (M::kRing + kStages * M::kMeta + M::kScales) + w * M::kQueries;
-    mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
 
-    // Steps are looked up ahead of their copies, so that no copy waits for a table: while one
-    // step is copied, the page numbers of the next (n_*) and the list entries of the one
-    // after it (a cursor) are on their way. Lane t < kSub looks after 16-key tile t.
-    Cursor ac = cc;
+    // Page numbers are looked up for a batch of steps of one segment at a time (lane = step of
+    // the batch x tile of the step), one step ahead of their first use: no copy waits for a
+    // table but the first.
+    constexpr int kBatch = 32 / M::kSub;
+    Cursor ac = cc;                      // first step of the batch
     const int in_page = (1 << p.c.page_log2) - 1;
-    int a_lp = 0, n_pos = kNoPos, n_pg = 0, n_h = 0, n_len = 0;
-    int to_list = steps, to_table = steps, to_issue = steps;
-    auto list = [&]() {        // logical page of the cursor's tile
-      if (--to_list < 0) return;
+    int b_n = 0, b_i = 0, b_pos = 0, b_pg = 0, left = steps;   // left: steps from the batch's first on
+    auto look_up = [&]() {
+      b_n = min(min(kBatch, left), ac.x.n - ac.s);
+      b_i = 0;
+      b_pos = kNoPos;
+      b_pg = 0;
       const int vi = ac.s * M::kKeys + lane * 16;
-      a_lp = -1;
-      if (lane < M::kSub && vi < ac.x.keys) {
-        a_lp = vi >> p.c.page_log2;
-        if (p.kv_idx) a_lp = p.kv_idx[((int64_t)ac.b * p.c.H + ac.h) * p.cap + a_lp];
-      }
-    };
-    auto table = [&]() {       // its page number and position; then on to the next step
-      if (--to_table < 0) return;
-      n_h = ac.h;
-      n_len = ac.x.len;
-      n_pos = kNoPos;
-      if ((unsigned)a_lp < (unsigned)p.c.table_width) {
-        const int at = (a_lp << p.c.page_log2) + ((ac.s * M::kKeys + lane * 16) & in_page);
-        if (at < n_len) {
-          n_pos = at;
-          n_pg = p.c.table[ac.b * p.c.table_stride + a_lp];
+      if (lane < b_n * M::kSub && vi < ac.x.keys) {
+        int lp = vi >> p.c.page_log2;
+        if (p.kv_idx) lp = p.kv_idx[((int64_t)ac.b * p.c.H + ac.h) * p.cap + lp];
+        if ((unsigned)lp < (unsigned)p.c.table_width) {
+          const int at = (lp << p.c.page_log2) + (vi & in_page);
+          if (at < ac.x.len) {
+            b_pos = at;
+            b_pg = p.c.table[ac.b * p.c.table_stride + lp];
+          }
         }
       }
-      if (to_table > 0) next_step<M>(p, ac, R);
     };
     const uint32_t lane_off = M::lane_part(lane);
     const int lane_row = lane / M::kChunks;
@@ -779,19 +853,22 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
     const uint8_t* kbase = static_cast<const uint8_t*>(p.c.k) + lane * 16;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.c.v) + lane * 16;
     auto issue = [&](int st) {
-      if (--to_issue >= 0) {
+      if (left > 0) {
         const uint32_t kdst = smem_u32(ring + st * 8192);
         uint8_t* meta = metas + st * M::kMeta;
-        if (n_pos != kNoPos && (unsigned)n_pg >= (unsigned)p.c.num_pages) {
-          n_pos = kNoPos;
+        if (b_i == 0 && b_pos != kNoPos && (unsigned)b_pg >= (unsigned)p.c.num_pages) {
+          b_pos = kNoPos;
           if (p.c.err_flag) atomicOr(p.c.err_flag, SA_FLAG_INDEX_BIT);
         }
-        if (lane < M::kSub) reinterpret_cast<int*>(meta + 128)[lane] = n_pos;
-        const int pos0 = __shfl_sync(~0u, n_pos, 0), pg0 = __shfl_sync(~0u, n_pg, 0);
-        if (in_page + 1 >= M::kKeys && n_len - pos0 >= M::kKeys) {
+        const int first = b_i * M::kSub;
+        if (M::kSub == 1 ? lane == first : lane - first >= 0 && lane - first < M::kSub)
+          reinterpret_cast<int*>(meta + 128)[lane - first] = b_pos;
+        const int pos0 = __shfl_sync(~0u, b_pos, first), pg0 = __shfl_sync(~0u, b_pg, first);
+        const uint32_t hrow = (uint32_t)ac.h << p.c.page_log2;
+        if (in_page + 1 >= M::kKeys && ac.x.len - pos0 >= M::kKeys) {
           // the whole step lies in one page
-          const uint32_t row = ((uint32_t)n_h << p.c.page_log2) + (pos0 & in_page);
-          const uint64_t at = (uint64_t)(uint32_t)pg0 * page_bytes + (uint64_t)row * M::kRow;
+          const uint64_t at = (uint64_t)(uint32_t)pg0 * page_bytes +
+                              (uint64_t)(hrow + (pos0 & in_page)) * M::kRow;
           const uint8_t* ks = kbase + at;
           const uint8_t* vs = vbase + at;
 #pragma unroll
@@ -810,10 +887,11 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
         } else {
 #pragma unroll 1
           for (int t = 0; t < M::kSub; ++t) {
-            const int pos = __shfl_sync(~0u, n_pos, t), pg = __shfl_sync(~0u, n_pg, t);
-            const int live = n_len - pos;     // rows of the tile that exist (< 0: no tile)
-            const uint32_t row = ((uint32_t)n_h << p.c.page_log2) + (pos & in_page);
-            const uint64_t at = live > 0 ? (uint64_t)(uint32_t)pg * page_bytes + (uint64_t)row * M::kRow : 0;
+            const int pos = __shfl_sync(~0u, b_pos, first + t), pg = __shfl_sync(~0u, b_pg, first + t);
+            const int live = ac.x.len - pos;     // rows of the tile that exist (< 0: no tile)
+            const uint64_t at = live > 0 ? (uint64_t)(uint32_t)pg * page_bytes +
+                                               (uint64_t)(hrow + (pos & in_page)) * M::kRow
+                                         : 0;
             // rows behind the last one are zeros here, whatever the page holds
 #pragma unroll
             for (int i = 0; i < M::kChunks / 2; ++i) {
@@ -829,14 +907,19 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
             }
           }
         }
-        table();
-        list();
+        if (++b_i == b_n) {
+          left -= b_n;
+          if (left > 0) {
+            advance<M>(p, ac, b_n, R);
+            look_up();
+          }
+        }
       }
       cp_async_commit();
     };
-    list();
-    table();
-    list();
+    if constexpr (!M::kQs) mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
+    look_up();
+    if constexpr (M::kQs) mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
 #pragma unroll 1
     for (int st = 0; st < kStages; ++st) issue(st);
 
@@ -864,7 +947,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
       __syncwarp();
       const bool ends = cc.s + 1 == cc.x.n, last = i + 1 == steps;
       if (ends || last) {
-        const bool whole = ends && seg0 >= lo;
+        const bool whole = !CLUSTER && ends && seg0 >= lo;
         const int rows = min(M::kRows, R - cc.r0);
         const int64_t row0 = ((int64_t)cc.b * p.Hq + cc.h * G) * p.T + cc.r0;
         float* slot = reinterpret_cast<float*>(ring);       // the partial at the share's end
@@ -899,7 +982,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
           e_at[2 * w + (last ? 1 : 0)] = Place{cc.b, cc.h, cc.r0, cc.x.n, seg0};
       }
       if (!last) {
-        next_step<M>(p, cc, R);
+        advance<M>(p, cc, 1, R);
         issue(st);
         if (ends) {
           seg0 = lo + i + 1;
@@ -913,75 +996,96 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
   __syncthreads();
 
   // ---- join the partials of each segment that several warps of this CTA shared
-  if (tid == 0) rec->at.b = -1;
-  // weights of the partials: entry e's row r against the largest maximum of its segment
-  for (int x = tid; x < 2 * kWarps * M::kRows; x += kThreads) {
-    const int e = x / M::kRows, r = x % M::kRows;
-    if (e_at[e].b < 0) continue;
-    const long long s0 = e_at[e].s0;
-    float mx = -INFINITY;
-    bool first = true;
-    for (int k = 0; k < 2 * kWarps; ++k)
-      if (e_at[k].b >= 0 && e_at[k].s0 == s0) {
-        mx = fmaxf(mx, s_ml[k][0][r]);
-        first &= k >= e;
-      }
-    s_w[e][r] = ex2a(s_ml[e][0][r] - ref_of(mx));
-    if (!first) continue;
-    float ls = 0.f;
-    for (int k = e; k < 2 * kWarps; ++k)
-      if (e_at[k].b >= 0 && e_at[k].s0 == s0) ls += ex2a(s_ml[k][0][r] - ref_of(mx)) * s_ml[k][1][r];
-    s_max[e][r] = mx;
-    s_sum[e][r] = ls;
-  }
-  __syncthreads();
-  for (int e0 = 0; e0 < 2 * kWarps;) {
+  if (!CLUSTER && tid == 0) rec->at.b = -1;
+  // Lane e of every warp looks at partial e: mask, the partials of its segment. They are the
+  // end partials of neighbouring warps and at most one head partial, the last of them.
+  const long long e_s0 = lane < 2 * kWarps && e_at[lane].b >= 0 ? e_at[lane].s0 : -1 - lane;
+  const uint32_t e_mask = __match_any_sync(~0u, e_s0);
+  uint32_t todo = __ballot_sync(~0u, e_s0 >= 0 && __ffs(e_mask) - 1 == lane);
+  for (; todo; todo &= todo - 1) {
+    const int e0 = __ffs(todo) - 1;
+    const uint32_t mask = __shfl_sync(~0u, e_mask, e0);
     const Place at = e_at[e0];
-    if (at.b < 0) {
-      ++e0;
-      continue;
-    }
-    int e1 = e0 + 1;
-    while (e1 < 2 * kWarps && (e_at[e1].b < 0 || e_at[e1].s0 == at.s0)) ++e1;
-    uint32_t mask = 0;         // the segment's partials
-    for (int e = e0; e < e1; ++e) mask |= (e_at[e].b >= 0 ? 1u : 0u) << e;
+    const int hd = __ffs(mask & 0x55555555u) - 1;      // the head partial, -1: none
     const int rows = min(M::kRows, R - at.r0);
-    const bool whole = at.s0 >= lo_c && at.s0 + at.n <= hi_c;
+    const bool whole = !CLUSTER && at.s0 >= lo_c && at.s0 + at.n <= hi_c;
     const int64_t row0 = ((int64_t)at.b * p.Hq + at.h * G) * p.T + at.r0;
-    float* dst = cta_slots + ((size_t)blockIdx.x * 2 + (at.s0 < lo_c ? 0 : 1)) * kSlot;
+    float* dst = CLUSTER ? s_cta : cta_slots + ((size_t)blockIdx.x * 2 + (at.s0 < lo_c ? 0 : 1)) * kSlot;
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), c = x % (D / 4) * 4;
+      float wt[kWarps], mx = -INFINITY, ls = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 2 * kWarps; ++e) {
-        if (!(mask >> e & 1)) continue;
-        const float* s = (e & 1) ? reinterpret_cast<const float*>(smem + (size_t)(e >> 1) * M::kRing) + r * M::kPad
-                                 : heads + ((size_t)blockIdx.x * kWarps + (e >> 1)) * kSlot + r * D;
-        const float a = s_w[e][r];
-        const float4 v = *reinterpret_cast<const float4*>(s + c);
+      for (int i = 0; i < kWarps; ++i) {
+        wt[i] = mask >> (2 * i + 1) & 1 ? s_ml[2 * i + 1][0][r] : -INFINITY;
+        mx = fmaxf(mx, wt[i]);
+      }
+      if (hd >= 0) {
+        const float mh = s_ml[hd][0][r];
+        mx = fmaxf(mx, mh);
+        const float a = ex2a(mh - ref_of(mx));
+        const float4 v = *reinterpret_cast<const float4*>(
+            heads + ((size_t)blockIdx.x * kWarps + (hd >> 1)) * kSlot + r * D + c);
+        ls = a * s_ml[hd][1][r];
+        y = make_float4(a * v.x, a * v.y, a * v.z, a * v.w);
+      }
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (!(mask >> (2 * i + 1) & 1)) continue;
+        const float a = ex2a(wt[i] - ref_of(mx));
+        const float4 v = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem + (size_t)i * M::kRing) + r * M::kPad + c);
+        ls += a * s_ml[2 * i + 1][1][r];
         y.x += a * v.x;
         y.y += a * v.y;
         y.z += a * v.z;
         y.w += a * v.w;
       }
-      const float ls = s_sum[e0][r];
       if (whole) {
         const float inv = ls == 0.f ? 0.f : 1.f / ls;
         put4(p, row0 + r, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-        if (c == 0) put_lse(p, row0 + r, s_max[e0][r], ls);
+        if (c == 0) put_lse(p, row0 + r, mx, ls);
       } else {
         *reinterpret_cast<float4*>(dst + r * D + c) = y;
         if (c == 0) {
-          dst[M::kRows * D + r] = s_max[e0][r];
+          dst[M::kRows * D + r] = mx;
           dst[M::kRows * D + M::kRows + r] = ls;
         }
       }
     }
-    if (!whole && at.s0 >= lo_c && tid == 0) {
+    if (!CLUSTER && !whole && at.s0 >= lo_c && tid == 0) {
       rec->at = at;
-      rec->last = cut.share_of(at.s0 + at.n - 1);
+      rec->last = Cut(total, ctas).share_of(at.s0 + at.n - 1);
     }
-    e0 = e1;
+  }
+
+  if constexpr (CLUSTER) {
+    // ---- and of the cluster's CTAs: each joins its share of the rows
+    const int size = units, rank = (int)cluster_rank(), used = min(size, cc.x.n);
+    cluster_sync();
+    const int rows = min(M::kRows, R - cc.r0);
+    const int64_t row0 = ((int64_t)cc.b * p.Hq + cc.h * G) * p.T + cc.r0;
+    for (int x = rank * kThreads + tid; x < rows * (D / 4); x += size * kThreads) {
+      const int r = x / (D / 4), c = x % (D / 4) * 4;
+      float mx = -INFINITY, ls = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < used; ++k)
+        mx = fmaxf(mx, peer_f32(peer_addr(s_cta + M::kRows * D + r, k)));
+#pragma unroll 4
+      for (int k = 0; k < used; ++k) {
+        const float a = ex2a(peer_f32(peer_addr(s_cta + M::kRows * D + r, k)) - ref_of(mx));
+        const float4 v = peer_f32x4(peer_addr(s_cta + r * D + c, k));
+        ls += a * peer_f32(peer_addr(s_cta + M::kRows * D + M::kRows + r, k));
+        y.x += a * v.x;
+        y.y += a * v.y;
+        y.z += a * v.z;
+        y.w += a * v.w;
+      }
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      put4(p, row0 + r, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+      if (c == 0) put_lse(p, row0 + r, mx, ls);
+    }
+    cluster_sync();   // no CTA leaves while another reads its shared memory
   }
 }
 
@@ -1047,40 +1151,90 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs p, int ctas
   }
 }
 
-template <int D, class M>
-cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
-  const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  const int groups = (int)((R + M::kRows - 1) / M::kRows);
-  const int units = p.kv_idx ? p.B * p.c.H : p.B;
-  // never more CTAs than a table full of keys gives every warp a step
-  const long long most = (long long)p.B * p.c.H * groups *
-                         (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) /
-                              M::kKeys + 1);
-  const int ctas = (int)std::min<long long>(p.sms, (most + M::kWarps - 1) / M::kWarps);
-  auto* kern = decode_kernel<D, M>;
-  static std::atomic<bool> ready[64];   // per device: the shared-memory limit is raised
+// Raises a kernel's shared-memory limit, once per device.
+template <class K>
+cudaError_t allow_smem(K* kern, size_t bytes, std::atomic<bool> (&ready)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)M::kSmem);
+  if (dev >= 0 && dev < 64 && ready[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+// Clusters of 2, 4 or 8 CTAs that the current device runs at the same time; asked once.
+template <class K>
+cudaError_t clusters_at_once(K* kern, const cudaLaunchConfig_t& cfg, int size, int& n,
+                             std::atomic<int> (&cache)[64][4]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int log2 = size == 2 ? 1 : size == 4 ? 2 : 3;
+  if (dev >= 0 && dev < 64 && (n = cache[dev][log2].load(std::memory_order_relaxed)) > 0)
+    return cudaSuccess;
+  e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev][log2].store(n, std::memory_order_relaxed);
+  return e;
+}
+
+template <int D, class M>
+cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
+  static std::atomic<bool> ready_line[64], ready_cluster[64];
+  static std::atomic<int> resident[64][4];
+  const long long R = (long long)(p.Hq / p.c.H) * p.T;
+  const int groups = (int)((R + M::kRows - 1) / M::kRows);
+  const long long segs = (long long)p.B * p.c.H * groups;
+  // steps of a segment whose table row (or list) is full
+  const long long most =
+      (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) + M::kKeys - 1) / M::kKeys;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.blockDim = dim3(M::kThreads);
+  cfg.dynamicSmemBytes = M::kSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+
+  // A cluster per segment where all clusters run at once and that gives the SMs about as much
+  // work as the line would: see kClusterSlack.
+  int size = 8;
+  while (size > 1 && segs * size > p.sms) size /= 2;
+  const long long on_line = (segs * most + (long long)p.sms * M::kWarps - 1) / ((long long)p.sms * M::kWarps);
+  for (; size >= 1 && segs * size <= p.sms; size /= 2) {
+    const long long in_cluster = (most + size * M::kWarps - 1) / (size * M::kWarps);
+    if (in_cluster > on_line + kClusterSlack) break;
+    auto* kern = decode_kernel<D, M, true>;
+    cudaError_t e = allow_smem(kern, M::kSmem, ready_cluster);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+    cfg.gridDim = dim3((unsigned)(segs * size));
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    int at_once = 0;
+    if (size > 1) {
+      e = clusters_at_once(kern, cfg, size, at_once, resident);
+      if (e != cudaSuccess) return e;
+      if (segs > at_once) continue;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, p, size, groups);
   }
+
+  const int units = p.kv_idx ? p.B * p.c.H : p.B;
+  // never more CTAs than full tables give every warp a step
+  const int ctas = (int)std::min<long long>(p.sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
+  auto* kern = decode_kernel<D, M, false>;
+  cudaError_t e = allow_smem(kern, M::kSmem, ready_line);
+  if (e != cudaSuccess) return e;
   kern<<<ctas, M::kThreads, M::kSmem, st>>>(p, units, groups);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int rows = (int)std::min<long long>(R, M::kRows);
   // set up while the main kernel runs; it waits for that kernel's end before it reads
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, rows);
+  cfg.gridDim = dim3(ctas, (unsigned)std::min<long long>(R, M::kRows));
   cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
+  cfg.dynamicSmemBytes = 0;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, M::kRows, M::kWarps>, p, ctas);
 }
 
