@@ -688,20 +688,39 @@ int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_
   if (int rc = check_device()) return rc;
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
-  if (sa::decode_work_bytes(B, Hq, Hkv, T, d, sms)) SA_REQUIRE_PTR(work);
   sa::DecodeArgs p{c, q, qs, B, Hq, T, lens, kv_idx, kv_cnt, cap, scale, sms, work, out, out_dtype,
                    lse};
+  size_t need = 0;
+  if (cudaError_t e = sa::decode_work_bytes(p, &need)) return launched(e, "decode plan");
+  if (need) SA_REQUIRE_PTR(work);
   return launched(sa::launch_decode(p, static_cast<cudaStream_t>(stream)), "decode launch");
 }
 
-int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms, size_t* bytes) {
+int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int cache_dtype, int page,
+                                  int table_width, int cap, int out_dtype, size_t* bytes) {
   if (int rc = check_decode_shape(B, Hq, Hkv, T, d)) return rc;
   SA_REQUIRE(bytes != nullptr, "bytes must be non-null");
-  SA_REQUIRE(sms >= 0, "sms must be >= 0");
-  if (sms == 0)
-    if (int rc = sm_count(&sms)) return rc;
-  *bytes = (long long)B * Hq == 0 ? 0 : sa::decode_work_bytes(B, Hq, Hkv, T, d, sms);
-  return ok();
+  SA_REQUIRE(cap >= -1 && (long long)cap * page <= 1 << 30, "cap must be >= -1 and cap * page <= 2^30");
+  SA_REQUIRE(out_dtype == SA_OUT_F32 || out_dtype == SA_OUT_BF16, "out_dtype must be F32 or BF16");
+  sa::PagedView c;
+  if (int rc = paged_view(&c, nullptr, nullptr, nullptr, nullptr, cache_dtype, 0, page, nullptr,
+                          table_width, table_width, B, Hkv, d, 0, nullptr))
+    return rc;
+  *bytes = 0;
+  if ((long long)B * Hq == 0) return ok();
+  if (int rc = check_device()) return rc;
+  sa::DecodeArgs p{};
+  p.c = c;
+  p.B = B;
+  p.Hq = Hq;
+  p.T = T;
+  static const int32_t lists = 0;          // stands for lists; not read
+  p.kv_idx = cap >= 0 ? &lists : nullptr;
+  p.cap = cap;
+  p.out_dtype = out_dtype;
+  if (int rc = sm_count(&p.sms)) return rc;
+  const cudaError_t e = sa::decode_work_bytes(p, bytes);
+  return launched(e, "decode plan");
 }
 
 }  // extern "C"

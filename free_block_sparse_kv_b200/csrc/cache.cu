@@ -2,29 +2,45 @@
 // cached rows back into contiguous bf16.
 //
 // Both are one pass over the rows: their floor is the rows read and written once at the
-// copy rate. A row's d values belong to d/8 neighbouring lanes (append) or d/16 (8-bit
-// read), so that the row's largest magnitude is a few shuffles and nothing is staged.
+// copy rate. A row's d values belong to d/8 neighbouring lanes, so that the row's largest
+// magnitude is a few shuffles and nothing is staged.
+#include <algorithm>
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace sa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;  // rows of K and of V in flight per thread
+constexpr int kUnroll = 2;      // rows of K and of V in flight per thread, append
+constexpr int kReadUnroll = 4;  // and read
+constexpr int kReadBlocks = 148 * 16;   // blocks of a read that has work for them
 
-// The row's largest finite magnitude as bf16 bits, over the LPR lanes that share the row.
+// The row's largest magnitude as bf16 bits, over the LPR lanes that share the row.
 template <int LPR>
 SA_DEVI uint32_t row_top(const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7FFF7FFFu;
-    top = __vmaxu2(top, a & ~__vcmpgeu2(a, 0x7F807F80u));  // infinities and NaN left out
-  }
+  uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                          __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
   return max(top & 0xFFFFu, top >> 16);
+}
+
+constexpr uint32_t kInf = 0x7F80u;
+
+// A row with infinities or NaN (rare): zeros in their places for the scale (NANS false), or
+// NaN in the places of infinities for the codes.
+template <bool NANS>
+SA_DEVI uint4 without_inf(uint4 x) {
+  uint32_t* w = &x.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if ((w[i] >> (16 * j) & 0x7FFFu) >= kInf)
+        w[i] = NANS ? w[i] | 0x7FFFu << (16 * j) : w[i] & ~(0xFFFFu << (16 * j));
+  return x;
 }
 
 // E8M0 of the smallest power of two s with top / s <= 448 = 1.75 * 2^8: the exponent of
@@ -36,19 +52,28 @@ SA_DEVI uint32_t row_scale(uint32_t top) {
   return (uint32_t)max(e, 1);
 }
 
-// Four bf16 pairs * 2^(127 - s) -> eight e4m3 codes; infinities become NaN codes.
+// Four bf16 pairs * 2^(127 - s) -> eight e4m3 codes.
 SA_DEVI uint2 row_codes(const uint4& x, uint32_t s) {
   const float inv = __uint_as_float((254u - s) << 23);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t bad = __vcmpgeu2(w[i] & 0x7FFF7FFFu, 0x7F807F80u);
-    const uint32_t v = w[i] | (bad & 0x7FFF7FFFu);
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(v) * inv, bf16_hi(v) * inv),
+  for (int i = 0; i < 4; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv),
                                     __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+}
+
+// Scale and codes of a row (each lane its part). Every lane of the warp calls.
+template <int LPR>
+SA_DEVI uint2 quantise(uint4 x, uint32_t& s) {
+  uint32_t top = row_top<LPR>(x);
+  if (__any_sync(~0u, top >= kInf)) {
+    top = row_top<LPR>(without_inf<false>(x));
+    x = without_inf<true>(x);
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  s = row_scale(top);
+  return row_codes(x, s);
 }
 
 template <int D, bool E4M3>
@@ -90,10 +115,11 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendArgs 
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     if constexpr (E4M3) {
-      const uint32_t ks = row_scale(row_top<LPR>(kx[u])), vs = row_scale(row_top<LPR>(vx[u]));
+      uint32_t ks, vs;
+      const uint2 kc = quantise<LPR>(kx[u], ks), vc = quantise<LPR>(vx[u], vs);
       if (dst[u] < 0) continue;
-      reinterpret_cast<uint2*>(p.c.k)[dst[u] * LPR + lane] = row_codes(kx[u], ks);
-      reinterpret_cast<uint2*>(p.c.v)[dst[u] * LPR + lane] = row_codes(vx[u], vs);
+      reinterpret_cast<uint2*>(p.c.k)[dst[u] * LPR + lane] = kc;
+      reinterpret_cast<uint2*>(p.c.v)[dst[u] * LPR + lane] = vc;
       if (lane == 0) {
         p.c.k_scale[dst[u]] = (uint8_t)ks;
         p.c.v_scale[dst[u]] = (uint8_t)vs;
@@ -106,25 +132,27 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendArgs 
   }
 }
 
-// Sixteen e4m3 codes times the row's scale -> sixteen bf16 (two 16-byte words).
-SA_DEVI void row_values(const uint4& x, float s, uint4 out[2]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t y[8];
+// Eight e4m3 codes times the row's scale -> eight bf16.
+SA_DEVI uint4 row_values(const uint2& x, float s) {
+  const uint32_t w[2] = {x.x, x.y};
+  uint32_t y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t h = e4m3x2_to_f16x2(w[i] >> (16 * j));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
       y[2 * i + j] = pack_bf16(f.x * s, f.y * s);
     }
-  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+// A block takes every gridDim.x-th tile of a sequence's rows, counted from its first one: how
+// many rows there are is known on the device only.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadArgs p) {
-  constexpr int LPR = E4M3 ? D / 16 : D / 8, RPP = kThreads / LPR;
+  constexpr int LPR = D / 8, RPP = kThreads / LPR;
+  using Word = std::conditional_t<E4M3, uint2, uint4>;    // a lane's eight values as they are held
   const int h = blockIdx.y, b = blockIdx.z;
   int n = seq_len(p.c, p.lens, b), f = p.first ? p.first[b] : 0;
   if (n > p.N || f < 0) {
@@ -132,44 +160,41 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadArgs p) {
     n = min(n, p.N);
     f = max(f, 0);
   }
-  const int page = 1 << p.c.page_log2, lane = threadIdx.x % LPR;
-  const int64_t t0 = (int64_t)blockIdx.x * (RPP * kUnroll) + threadIdx.x / LPR;
-  uint4 kx[kUnroll], vx[kUnroll];
-  float ks[kUnroll], vs[kUnroll];
-  bool live[kUnroll];
+  const int in_page = (1 << p.c.page_log2) - 1, lane = threadIdx.x % LPR;
+  uint16_t* kd = p.k + b * p.ks.b + h * p.ks.h + lane * 8;
+  uint16_t* vd = p.v + b * p.vs.b + h * p.vs.h + lane * 8;
+  for (int64_t t0 = f + (int64_t)blockIdx.x * (RPP * kReadUnroll) + threadIdx.x / LPR; t0 < n;
+       t0 += (int64_t)gridDim.x * (RPP * kReadUnroll)) {
+    Word kx[kReadUnroll], vx[kReadUnroll];
+    float ks[kReadUnroll], vs[kReadUnroll];
+    int pg[kReadUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t t = t0 + u * RPP;
-    live[u] = false;
-    if (t < f || t >= n) continue;
-    const int pg = pool_page(p.c, b, (int)(t >> p.c.page_log2));
-    if (pg < 0) continue;
-    live[u] = true;
-    const int64_t src = (((int64_t)pg * p.c.H + h) << p.c.page_log2) + (t & (page - 1));
-    kx[u] = __ldg(reinterpret_cast<const uint4*>(p.c.k) + src * LPR + lane);
-    vx[u] = __ldg(reinterpret_cast<const uint4*>(p.c.v) + src * LPR + lane);
-    if (E4M3) {
-      ks[u] = e8m0_value(p.c.k_scale[src]);
-      vs[u] = e8m0_value(p.c.v_scale[src]);
+    for (int u = 0; u < kReadUnroll; ++u) {
+      const int64_t t = t0 + u * RPP;
+      pg[u] = t < n ? pool_page(p.c, b, (int)(t >> p.c.page_log2)) : -1;
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (!live[u]) continue;
-    const int64_t t = t0 + u * RPP;
-    uint4* kd = reinterpret_cast<uint4*>(p.k + b * p.ks.b + h * p.ks.h + t * p.ks.t);
-    uint4* vd = reinterpret_cast<uint4*>(p.v + b * p.vs.b + h * p.vs.h + t * p.vs.t);
-    if constexpr (E4M3) {
-      uint4 y[2];
-      row_values(kx[u], ks[u], y);
-      kd[2 * lane] = y[0];
-      kd[2 * lane + 1] = y[1];
-      row_values(vx[u], vs[u], y);
-      vd[2 * lane] = y[0];
-      vd[2 * lane + 1] = y[1];
-    } else {
-      kd[lane] = kx[u];
-      vd[lane] = vx[u];
+    for (int u = 0; u < kReadUnroll; ++u) {
+      if (pg[u] < 0) continue;
+      const int64_t src = (((int64_t)pg[u] * p.c.H + h) << p.c.page_log2) + ((t0 + u * RPP) & in_page);
+      kx[u] = __ldg(reinterpret_cast<const Word*>(p.c.k) + src * LPR + lane);
+      vx[u] = __ldg(reinterpret_cast<const Word*>(p.c.v) + src * LPR + lane);
+      if constexpr (E4M3) {
+        ks[u] = e8m0_value(p.c.k_scale[src]);
+        vs[u] = e8m0_value(p.c.v_scale[src]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadUnroll; ++u) {
+      if (pg[u] < 0) continue;
+      const int64_t t = t0 + u * RPP;
+      if constexpr (E4M3) {
+        *reinterpret_cast<uint4*>(kd + t * p.ks.t) = row_values(kx[u], ks[u]);
+        *reinterpret_cast<uint4*>(vd + t * p.vs.t) = row_values(vx[u], vs[u]);
+      } else {
+        *reinterpret_cast<uint4*>(kd + t * p.ks.t) = kx[u];
+        *reinterpret_cast<uint4*>(vd + t * p.vs.t) = vx[u];
+      }
     }
   }
 }
@@ -185,8 +210,10 @@ cudaError_t append_t(const CacheAppendArgs& p, cudaStream_t st) {
 
 template <int D, bool E4M3>
 cudaError_t read_t(const CacheReadArgs& p, cudaStream_t st) {
-  constexpr int per = kThreads / (E4M3 ? D / 16 : D / 8) * kUnroll;
-  const dim3 grid((unsigned)(((long long)p.N + per - 1) / per), (unsigned)p.c.H, (unsigned)p.B);
+  constexpr int per = kThreads / (D / 8) * kReadUnroll;
+  const long long bh = (long long)p.B * p.c.H, tiles = (p.N + per - 1) / per;
+  const long long share = (kReadBlocks + bh - 1) / bh;
+  const dim3 grid((unsigned)std::min(tiles, share), (unsigned)p.c.H, (unsigned)p.B);
   cache_read_kernel<D, E4M3><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -35,13 +35,15 @@
 namespace sa {
 namespace {
 
-constexpr int kMaxWarps = 16;
 constexpr int kLaneUnits = 8;
 // A cluster per segment saves the scan, the partials' way through memory and the second
 // kernel, about as long as this many steps of a warp take.
 constexpr long long kClusterSlack = 4;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
-constexpr float kShift16 = 14.f;       // f16 weights are at most 2^14 (fp16 ends at 2^16)
+// The level that a column's weights are relative to follows its running maximum only when that
+// has grown by more than this (base 2): most steps then rescale nothing.
+constexpr float kSlack = 4.f;
+constexpr float kShift16 = 10.f;       // f16 weights are at most 2^(10 + kSlack) (fp16 ends at 2^16)
 
 // A segment: its sequence, kv head and first query row, its steps, and where it starts on the
 // line (which tells segments apart).
@@ -198,14 +200,17 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   static constexpr int kRows = 8 * NT, kMt = D / 16;
   // With 32 rows the queries would take 64 registers of a lane: they stay in shared memory.
   static constexpr bool kQs = NT == 4;
-  static constexpr int kQueries = kQs ? kRows * D * 2 : 0;
+  // With eight the next segment's are fetched there ahead of their use.
+  static constexpr bool kAhead = NT == 1;
+  static constexpr int kQueries = kQs || kAhead ? kRows * D * 2 : 0;
   // A warp's ring also takes its partial at the end of its share.
   static constexpr int kSlotBytes = kRows * L::kPad * 4;
   static constexpr int kRing = STAGES * 8192 > kSlotBytes ? STAGES * 8192 : (kSlotBytes + 255) / 256 * 256;
-  static constexpr size_t kSmem =
-      (size_t)WARPS * (kRing + STAGES * L::kMeta + L::kScales + kQueries) + 256;
+  static constexpr size_t smem(bool cluster) {   // a cluster's warps have one segment each
+    return (size_t)WARPS * (kRing + STAGES * L::kMeta + L::kScales + (cluster && !kQs ? 0 : kQueries)) + 256;
+  }
   uint32_t qf[kQs ? 1 : NT][D / 16][2];
-  uint32_t qs;                     // this warp's queries in shared memory (kQs)
+  uint32_t qs;                     // this warp's queries in shared memory (kQs, kAhead)
   int r0, len, R;
   float m[NT][2], l[NT][2], mv[NT][2], f[NT][2];
   int lim[NT][2];
@@ -260,18 +265,45 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     }
   }
 
+  // The next segment's queries into this warp's buffer, 16 bytes a lane; part of the next
+  // group of copies.
+  SA_DEVI void prefetch(const DecodeArgs& p, int b, int h, int r0_) const {
+    constexpr int CH = D / 8;
+    const int G = p.Hq / p.c.H, n = min(kRows, G * p.T - r0_) * CH;
+    for (int i = lane; i < n; i += 32) {
+      const int r = r0_ + i / CH, g = r / p.T, t = r - g * p.T;
+      const uint16_t* qp = p.q + b * p.qs.b + (int64_t)(h * G + g) * p.qs.h + t * p.qs.t + i % CH * 8;
+      cp_async16_whole(qs + swz(i / CH, i % CH, 2 * D), qp);
+    }
+  }
+  SA_DEVI void load_prefetched(const DecodeArgs& p, int r0_, int len_) {
+    R = p.Hq / p.c.H * p.T;
+    r0 = r0_;
+    len = len_;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // 4-byte word of the row: bf16 words 8 ks + q and + 4, e4m3 8 ks + 2q and + 1
+        const int word = 8 * ks + (E4M3 ? 2 * q4 + i : q4 + 4 * i);
+        uint32_t x = 0;
+        if (r0 + r8 < R)
+          asm volatile("ld.shared.b32 %0, [%1];\n"
+                       : "=r"(x) : "r"(qs + swz(r8, word >> 2, 2 * D) + (word & 3) * 4) : "memory");
+        qf[0][ks][i] = x;
+      }
+  }
   // The segment's queries are asked for, and (start) made operands once they are there.
   SA_DEVI void load(const DecodeArgs& p, int b, int h, int r0_, int len_) {
     R = p.Hq / p.c.H * p.T;
     r0 = r0_;
     len = len_;
     if constexpr (kQs) {
-#pragma unroll 1
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t x[D / 16][2];
-        fetch(p, b, h, nt, x);
-        store(nt, x);
-      }
+      uint32_t x[NT][D / 16][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) fetch(p, b, h, nt, x[nt]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) store(nt, x[nt]);
     } else {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) fetch(p, b, h, nt, qf[nt]);
@@ -336,6 +368,20 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         b[i][1] = qf[nt][2 * pair + i][1];
       }
     }
+  }
+
+  // No infinity or NaN among the V values of tile t.
+  SA_DEVI bool finite_values(const Step& w, int t) const {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < L::kChunks / 2; ++i) {
+      const uint4 y = *reinterpret_cast<const uint4*>(w.vp + t * 16 * L::kRow + (i * 32 + lane) * 16);
+      const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)    // all ones in an exponent carry into the sign's place
+        bad |= E4M3 ? (x[j] & 0x7F7F7F7Fu) + 0x01010101u : (x[j] & 0x7F807F80u) + 0x00800080u;
+    }
+    return !__any_sync(~0u, bad & (E4M3 ? 0x80808080u : 0x80008000u));
   }
 
   SA_DEVI void compute(const Step& w) {
@@ -413,7 +459,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
       }
     }
     // running maxima: the warp looks across its lanes, and rescales, only when one of its
-    // columns has a new one
+    // columns has outgrown its level
     float nm[NT][2], nv[NT][2];
     bool moved = false;
 #pragma unroll
@@ -429,8 +475,8 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         }
         nm[nt][i] = x;
         nv[nt][i] = y;
-        moved |= x > m[nt][i];
-        if constexpr (E4M3) moved |= y > mv[nt][i];
+        moved |= x > m[nt][i] + kSlack;
+        if constexpr (E4M3) moved |= y > mv[nt][i] + kSlack;
       }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -505,7 +551,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
                       a[i][2], a[i][3]);
         }
       };
-      if (w.all || !w.part(t)) {
+      if (w.all || !w.part(t) || finite_values(w, t)) {
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
           uint32_t a[2][4];
@@ -519,8 +565,8 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
             }
         }
       } else {
-        // New tokens that some rows attend and others do not: a zero weight times a
-        // non-finite value would reach the others, so each token's rows take a product
+        // New tokens that some rows attend and others do not, with a non-finite value: a
+        // zero weight times it would reach the others, so each token's rows take a product
         // of their own in which the values that they do not attend are zeros.
 #pragma unroll 1
         for (int tok = 0; tok < w.T; ++tok) {
@@ -569,21 +615,27 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         f[nt][k] = x;
       }
   }
-  // fn(row, m, l) for the rows of 8-row group g.
+  // fn(row, m, l) for the segment's rows.
   template <class F>
-  SA_DEVI void stats(int g, F fn) {
-    if (r8 == 0) {
-      fn(g * 8 + 2 * q4, m[g][0], l[g][0]);
-      fn(g * 8 + 2 * q4 + 1, m[g][1], l[g][1]);
-    }
+  SA_DEVI void stats(F fn) {
+    if (r8 == 0)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        fn(nt * 8 + 2 * q4, m[nt][0], l[nt][0]);
+        fn(nt * 8 + 2 * q4 + 1, m[nt][1], l[nt][1]);
+      }
   }
-  // The accumulators of 8-row group g as rows of kPad floats.
-  SA_DEVI void stage(int g, float* to) {
+  // fn(row, value column, numerator) for the lane's share: a warp's calls for one (mt, i) are
+  // eight neighbouring columns of four rows, whole 32-byte sectors of fp32.
+  template <class F>
+  SA_DEVI void emit(F fn) {
 #pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        to[(2 * q4 + (i & 1)) * L::kPad + 16 * mt + r8 + 8 * (i >> 1)] = o[mt][g][i] * f[g][i & 1];
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          fn(nt * 8 + 2 * q4 + (i & 1), 16 * mt + r8 + 8 * (i >> 1), o[mt][nt][i] * f[nt][i & 1]);
   }
 };
 
@@ -683,7 +735,7 @@ SA_DEVI float4 peer_f32x4(uint32_t a) {
 template <int D, class M, bool CLUSTER>
 __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, int units, int groups) {
   constexpr int kWarps = M::kWarps, kStages = M::kStages, kThreads = M::kThreads;
-  constexpr int kBuckets = kThreads;     // scan entries kept in shared memory
+  constexpr int kBuckets = 128;          // scan entries kept in shared memory
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long s_prefix[CLUSTER ? 1 : kBuckets + 1], s_warp[kWarps];
   // partials: of warp w, 2w at the head of its share, 2w + 1 at its end
@@ -730,7 +782,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
     per = by_warp ? (units + 31) / 32 : (units + kBuckets - 1) / kBuckets;
     const int first = (by_warp ? lane : tid) * per;
     bool none = false;
-    for (int u = first; u < min(units, first + per); ++u) {
+    for (int u = first; u < min(units, first + per) && (by_warp || tid < kBuckets); ++u) {
       const int n = unit_at(u).n;
       incl += (long long)n * segs;
       none |= n == 0;
@@ -754,7 +806,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
         if (i < w) before += s_warp[i];
         total += s_warp[i];
       }
-      s_prefix[tid] = before + incl - mine;
+      if (tid < kBuckets) s_prefix[tid] = before + incl - mine;
       if (tid == 0) s_prefix[kBuckets] = total;
       empty = __syncthreads_or(none);
     }
@@ -827,6 +879,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
     // table but the first.
     constexpr int kBatch = 32 / M::kSub;
     Cursor ac = cc;                      // first step of the batch
+    int seg_looked = 0, seg_begun = 0, seg_fetched = 0;   // segments after the first: counts
     const int in_page = (1 << p.c.page_log2) - 1;
     int b_n = 0, b_i = 0, b_pos = 0, b_pg = 0, left = steps;   // left: steps from the batch's first on
     auto look_up = [&]() {
@@ -892,6 +945,14 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
             const uint64_t at = live > 0 ? (uint64_t)(uint32_t)pg * page_bytes +
                                                (uint64_t)(hrow + (pos & in_page)) * M::kRow
                                          : 0;
+            if (live >= 16) {
+#pragma unroll
+              for (int i = 0; i < M::kChunks / 2; ++i) {
+                const uint32_t dst = kdst + t * 16 * M::kRow + M::piece(lane_off, i);
+                cp_async16_whole(dst, kbase + at + i * 512);
+                cp_async16_whole(dst + 4096, vbase + at + i * 512);
+              }
+            } else {
             // rows behind the last one are zeros here, whatever the page holds
 #pragma unroll
             for (int i = 0; i < M::kChunks / 2; ++i) {
@@ -899,6 +960,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
               const bool in = i * (32 / M::kChunks) + lane_row < live;
               cp_async16(dst, in ? kbase + at + i * 512 : kbase, in ? 16 : 0);
               cp_async16(dst + 4096, in ? vbase + at + i * 512 : vbase, in ? 16 : 0);
+            }
             }
             if constexpr (M::kE4M3) {
               if (lane < 2 && live > 0)
@@ -912,6 +974,12 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
           if (left > 0) {
             advance<M>(p, ac, b_n, R);
             look_up();
+            if constexpr (M::kAhead) {   // its buffer is free once the last segment asked for has begun
+              if (ac.s == 0 && ++seg_looked == seg_begun + 1) {
+                mth.prefetch(p, ac.b, ac.h, ac.r0);
+                seg_fetched = seg_looked;
+              }
+            }
           }
         }
       }
@@ -954,29 +1022,26 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
         if (last) cp_async_wait<0>();
         __syncwarp();
         mth.close(whole);
-#pragma unroll
-        for (int g = 0; g < M::kRows / 8; ++g) {
-          mth.stats(g, [&](int r, float m, float l) {
-            if (whole) {
-              if (r < rows) put_lse(p, row0 + r, m, l);
-            } else {
-              s_ml[2 * w + (last ? 1 : 0)][0][r] = m;
-              s_ml[2 * w + (last ? 1 : 0)][1][r] = l;
-            }
-          });
-          float* buf = !whole && last ? slot + g * 8 * M::kPad
-                                      : reinterpret_cast<float*>(ring + st * 8192);
-          mth.stage(g, buf);
-          if (whole || !last) {
-            __syncwarp();
-            for (int x = lane; x < min(8, rows - g * 8) * (D / 4); x += 32) {
-              const int r = x / (D / 4), c = x % (D / 4) * 4;
-              const float4 y = *reinterpret_cast<const float4*>(buf + r * M::kPad + c);
-              if (whole) put4(p, row0 + g * 8 + r, D, c, y);
-              else *reinterpret_cast<float4*>(head + (g * 8 + r) * D + c) = y;
-            }
-            __syncwarp();
+        mth.stats([&](int r, float m, float l) {
+          if (whole) {
+            if (r < rows) put_lse(p, row0 + r, m, l);
+          } else {
+            s_ml[2 * w + (last ? 1 : 0)][0][r] = m;
+            s_ml[2 * w + (last ? 1 : 0)][1][r] = l;
           }
+        });
+        if (whole) {
+          if (p.out_dtype == SA_OUT_F32) {
+            float* dst = static_cast<float*>(p.out) + row0 * D;
+            mth.emit([&](int r, int c, float y) { if (r < rows) dst[r * D + c] = y; });
+          } else {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row0 * D;
+            mth.emit([&](int r, int c, float y) { if (r < rows) dst[r * D + c] = __float2bfloat16(y); });
+          }
+        } else if (last) {
+          mth.emit([&](int r, int c, float y) { slot[r * M::kPad + c] = y; });
+        } else {
+          mth.emit([&](int r, int c, float y) { if (r < rows) head[r * D + c] = y; });
         }
         if (!whole && lane == 0)
           e_at[2 * w + (last ? 1 : 0)] = Place{cc.b, cc.h, cc.r0, cc.x.n, seg0};
@@ -986,8 +1051,11 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
         issue(st);
         if (ends) {
           seg0 = lo + i + 1;
-          mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
+          ++seg_begun;
+          if (M::kAhead && seg_fetched == seg_begun) mth.load_prefetched(p, cc.r0, cc.x.len);
+          else mth.load(p, cc.b, cc.h, cc.r0, cc.x.len);
           mth.start(p);
+          __syncwarp();
         }
         st = st + 1 == kStages ? 0 : st + 1;
       }
@@ -996,67 +1064,83 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
   __syncthreads();
 
   // ---- join the partials of each segment that several warps of this CTA shared
-  if (!CLUSTER && tid == 0) rec->at.b = -1;
-  // Lane e of every warp looks at partial e: mask, the partials of its segment. They are the
-  // end partials of neighbouring warps and at most one head partial, the last of them.
-  const long long e_s0 = lane < 2 * kWarps && e_at[lane].b >= 0 ? e_at[lane].s0 : -1 - lane;
-  const uint32_t e_mask = __match_any_sync(~0u, e_s0);
-  uint32_t todo = __ballot_sync(~0u, e_s0 >= 0 && __ffs(e_mask) - 1 == lane);
-  for (; todo; todo &= todo - 1) {
-    const int e0 = __ffs(todo) - 1;
-    const uint32_t mask = __shfl_sync(~0u, e_mask, e0);
+  // Lane e of every warp looks at partial e. A segment's partials are neighbours: the end
+  // partials of consecutive warps and at most one head partial, the last of them.
+  const bool valid = lane < 2 * kWarps && e_at[lane < 2 * kWarps ? lane : 0].b >= 0;
+  const int key = valid ? (int)(e_at[lane].s0 - lo_c) : 0;     // |s0 - lo_c| < 2^31: within a segment or share
+  const uint32_t held = __ballot_sync(~0u, valid), below = held & ((1u << lane) - 1u);
+  const int before = __shfl_sync(~0u, key, below ? 31 - __clz(below) : lane);
+  const uint32_t first = __ballot_sync(~0u, valid && (!below || before != key));
+  // The threads share out all segments' values, four of a row to a thread and round.
+  const int per_seg = min(M::kRows, R) * (D / 4), total_items = __popc(first) * per_seg;
+  uint32_t left = first;               // from the segment of the thread's item on
+  int x = tid;                         // and the item in it
+  for (int i0 = 0; i0 < total_items; i0 += kThreads, x += kThreads) {
+    while (x >= per_seg && left) {
+      x -= per_seg;
+      left &= left - 1;
+    }
+    if (!left) break;
+    const int e0 = __ffs(left) - 1;
+    const uint32_t next = left & (left - 1);
+    const uint32_t mask = held & (~0u << e0) & (next ? (1u << (__ffs(next) - 1)) - 1u : ~0u);
+    const int r = x / (D / 4), c = x % (D / 4) * 4;
     const Place at = e_at[e0];
+    if (r >= R - at.r0) continue;
     const int hd = __ffs(mask & 0x55555555u) - 1;      // the head partial, -1: none
-    const int rows = min(M::kRows, R - at.r0);
     const bool whole = !CLUSTER && at.s0 >= lo_c && at.s0 + at.n <= hi_c;
-    const int64_t row0 = ((int64_t)at.b * p.Hq + at.h * G) * p.T + at.r0;
-    float* dst = CLUSTER ? s_cta : cta_slots + ((size_t)blockIdx.x * 2 + (at.s0 < lo_c ? 0 : 1)) * kSlot;
-    for (int x = tid; x < rows * (D / 4); x += kThreads) {
-      const int r = x / (D / 4), c = x % (D / 4) * 4;
-      float wt[kWarps], mx = -INFINITY, ls = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float wt[kWarps], mx = -INFINITY, ls = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mh = -INFINITY, lh = 0.f;
+    if (hd >= 0) {
+      mh = s_ml[hd][0][r];
+      lh = s_ml[hd][1][r];
+      y = *reinterpret_cast<const float4*>(heads + ((size_t)blockIdx.x * kWarps + (hd >> 1)) * kSlot +
+                                           r * D + c);
+    }
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        wt[i] = mask >> (2 * i + 1) & 1 ? s_ml[2 * i + 1][0][r] : -INFINITY;
-        mx = fmaxf(mx, wt[i]);
-      }
-      if (hd >= 0) {
-        const float mh = s_ml[hd][0][r];
-        mx = fmaxf(mx, mh);
-        const float a = ex2a(mh - ref_of(mx));
-        const float4 v = *reinterpret_cast<const float4*>(
-            heads + ((size_t)blockIdx.x * kWarps + (hd >> 1)) * kSlot + r * D + c);
-        ls = a * s_ml[hd][1][r];
-        y = make_float4(a * v.x, a * v.y, a * v.z, a * v.w);
-      }
+    for (int i = 0; i < kWarps; ++i) {
+      wt[i] = mask >> (2 * i + 1) & 1 ? s_ml[2 * i + 1][0][r] : -INFINITY;
+      mx = fmaxf(mx, wt[i]);
+    }
+    mx = fmaxf(mx, mh);
+    const float ah = ex2a(mh - ref_of(mx));
+    ls = ah * lh;
+    y = make_float4(ah * y.x, ah * y.y, ah * y.z, ah * y.w);
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (!(mask >> (2 * i + 1) & 1)) continue;
-        const float a = ex2a(wt[i] - ref_of(mx));
-        const float4 v = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + (size_t)i * M::kRing) + r * M::kPad + c);
-        ls += a * s_ml[2 * i + 1][1][r];
-        y.x += a * v.x;
-        y.y += a * v.y;
-        y.z += a * v.z;
-        y.w += a * v.w;
-      }
-      if (whole) {
-        const float inv = ls == 0.f ? 0.f : 1.f / ls;
-        put4(p, row0 + r, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-        if (c == 0) put_lse(p, row0 + r, mx, ls);
-      } else {
-        *reinterpret_cast<float4*>(dst + r * D + c) = y;
-        if (c == 0) {
-          dst[M::kRows * D + r] = mx;
-          dst[M::kRows * D + M::kRows + r] = ls;
+    for (int i = 0; i < kWarps; ++i) {
+      const bool in = mask >> (2 * i + 1) & 1;
+      // (loaded in any case, so that the loads do not wait for one another)
+      const float4 v = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + (size_t)i * M::kRing) + r * M::kPad + c);
+      const float l = s_ml[2 * i + 1][1][r], a = ex2a(wt[i] - ref_of(mx));
+      ls += in ? a * l : 0.f;
+      y.x += in ? a * v.x : 0.f;
+      y.y += in ? a * v.y : 0.f;
+      y.z += in ? a * v.z : 0.f;
+      y.w += in ? a * v.w : 0.f;
+    }
+    if (whole) {
+      const int64_t row0 = ((int64_t)at.b * p.Hq + at.h * G) * p.T + at.r0;
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      put4(p, row0 + r, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+      if (c == 0) put_lse(p, row0 + r, mx, ls);
+    } else {
+      float* dst = CLUSTER ? s_cta : cta_slots + ((size_t)blockIdx.x * 2 + (at.s0 < lo_c ? 0 : 1)) * kSlot;
+      *reinterpret_cast<float4*>(dst + r * D + c) = y;
+      if (c == 0) {
+        dst[M::kRows * D + r] = mx;
+        dst[M::kRows * D + M::kRows + r] = ls;
+        if (!CLUSTER && r == 0 && at.s0 >= lo_c) {
+          rec->at = at;
+          rec->last = Cut(total, ctas).share_of(at.s0 + at.n - 1);
         }
       }
     }
-    if (!CLUSTER && !whole && at.s0 >= lo_c && tid == 0) {
-      rec->at = at;
-      rec->last = Cut(total, ctas).share_of(at.s0 + at.n - 1);
-    }
+  }
+  if (!CLUSTER && tid == 0) {   // no segment starts here and runs on: nothing to join
+    const Place at = first ? e_at[31 - __clz(first)] : Place{0, 0, 0, 0, 0};
+    if (!first || at.s0 < lo_c || at.s0 + at.n <= hi_c) rec->at.b = -1;
   }
 
   if constexpr (CLUSTER) {
@@ -1090,64 +1174,75 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
 }
 
 // Joins the partials of the segment that starts in CTA blockIdx.x's share and spans CTAs:
-// one block per row, its groups of D/4 threads take every eighth (or sixteenth) partial.
+// a block takes four rows, its groups of D/4 threads every eighth (or sixteenth) partial in
+// one pass with a running maximum, and then each other's sums.
 template <int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs p, int ctas_max) {
-  constexpr int LN = D / 4, GRP = 256 / LN;
-  __shared__ float red[8];
-  __shared__ float4 acc[256];
-  __shared__ float accl[GRP];
+  constexpr int LN = D / 4, GRP = 256 / LN, RB = 4;
+  __shared__ float4 acc[RB][256];
+  __shared__ float2 ml[RB][GRP];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the main kernel's partials are there
   const Record rec = static_cast<const Record*>(p.work)[blockIdx.x];
   if (rec.at.b < 0) return;
-  const int G = p.Hq / p.c.H, R = G * p.T, row = blockIdx.y, tid = threadIdx.x;
-  if (row >= R - rec.at.r0) return;
+  const int G = p.Hq / p.c.H, R = G * p.T, row0 = blockIdx.y * RB, tid = threadIdx.x;
+  const int rows = min(min(ROWS, R - rec.at.r0) - row0, RB);
+  if (rows <= 0) return;
   constexpr size_t kSlot = (size_t)ROWS * (D + 2);
   const float* slots = reinterpret_cast<const float*>(static_cast<const Record*>(p.work) + ctas_max) +
                        (size_t)ctas_max * WARPS * kSlot;
   // CTAs of the segment: blockIdx.x (slot 1), then those whose share starts inside it (slot 0)
-  const int parts = rec.last - blockIdx.x + 1;
-  auto slot = [&](int i) {
-    return slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
-  };
-  float M = -INFINITY;
-  for (int i = tid; i < parts; i += 256) M = fmaxf(M, slot(i)[ROWS * D + row]);
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-  if (tid % 32 == 0) red[tid / 32] = M;
-  __syncthreads();
-  for (int i = 0; i < 8; ++i) M = fmaxf(M, red[i]);
-  const int c = tid % LN * 4, grp = tid / LN;
-  float L = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp; i < parts; i += GRP) {
-    const float* s = slot(i);
-    const float a = ex2a(s[ROWS * D + row] - ref_of(M));
-    const float4 v = *reinterpret_cast<const float4*>(s + row * D + c);
-    L += a * s[ROWS * D + ROWS + row];
-    y.x += a * v.x;
-    y.y += a * v.y;
-    y.z += a * v.z;
-    y.w += a * v.w;
+  const int parts = rec.last - blockIdx.x + 1, c = tid % LN * 4, grp = tid / LN;
+  float mx[RB], ls[RB];
+  float4 y[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    mx[r] = -INFINITY;
+    ls[r] = 0.f;
+    y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  acc[tid] = y;
-  if (c == 0) accl[grp] = L;
-  __syncthreads();
-  if (grp == 0) {
-    L = 0.f;
-    y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int g = 0; g < GRP; ++g) {
-      const float4 v = acc[g * LN + tid];
-      L += accl[g];
-      y.x += v.x;
-      y.y += v.y;
-      y.z += v.z;
-      y.w += v.w;
+#pragma unroll 2
+  for (int i = grp; i < parts; i += GRP) {
+    const float* s = slots + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      if (r >= rows) continue;
+      const float m = s[ROWS * D + row0 + r], l = s[ROWS * D + ROWS + row0 + r];
+      const float4 v = *reinterpret_cast<const float4*>(s + (row0 + r) * D + c);
+      const float n = fmaxf(mx[r], m), e = ex2a(mx[r] - ref_of(n)), f = ex2a(m - ref_of(n));
+      mx[r] = n;
+      ls[r] = ls[r] * e + l * f;
+      y[r].x = y[r].x * e + v.x * f;
+      y[r].y = y[r].y * e + v.y * f;
+      y[r].z = y[r].z * e + v.z * f;
+      y[r].w = y[r].w * e + v.w * f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t orow = ((int64_t)rec.at.b * p.Hq + rec.at.h * G) * p.T + rec.at.r0 + row;
-    put4(p, orow, D, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-    if (c == 0) put_lse(p, orow, M, L);
+  }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    acc[r][tid] = y[r];
+    if (c == 0) ml[r][grp] = make_float2(mx[r], ls[r]);
+  }
+  __syncthreads();
+  for (int x = tid; x < rows * LN; x += 256) {
+    const int r = x / LN, k = x % LN;
+    float top = -INFINITY, sum = 0.f;
+    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < GRP; ++g) top = fmaxf(top, ml[r][g].x);
+#pragma unroll
+    for (int g = 0; g < GRP; ++g) {
+      const float f = ex2a(ml[r][g].x - ref_of(top));
+      const float4 v = acc[r][g * LN + k];
+      sum += f * ml[r][g].y;
+      z.x += f * v.x;
+      z.y += f * v.y;
+      z.z += f * v.z;
+      z.w += f * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t orow = ((int64_t)rec.at.b * p.Hq + rec.at.h * G) * p.T + rec.at.r0 + row0 + r;
+    put4(p, orow, D, k * 4, make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv));
+    if (k == 0) put_lse(p, orow, top, sum);
   }
 }
 
@@ -1178,21 +1273,24 @@ cudaError_t clusters_at_once(K* kern, const cudaLaunchConfig_t& cfg, int size, i
   return e;
 }
 
+// How a call of these sizes runs: clusters of `size` CTAs, or (size 0) `ctas` on the line.
+struct Plan {
+  int groups, size, ctas;
+  size_t bytes;   // scratch
+};
+
 template <int D, class M>
-cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
+cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, Plan& pl) {
   static std::atomic<bool> ready_line[64], ready_cluster[64];
   static std::atomic<int> resident[64][4];
   const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  const int groups = (int)((R + M::kRows - 1) / M::kRows);
-  const long long segs = (long long)p.B * p.c.H * groups;
+  pl = Plan{(int)((R + M::kRows - 1) / M::kRows), 0, 0, 0};
+  const long long segs = (long long)p.B * p.c.H * pl.groups;
   // steps of a segment whose table row (or list) is full
   const long long most =
       (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) + M::kKeys - 1) / M::kKeys;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
   cfg.blockDim = dim3(M::kThreads);
-  cfg.dynamicSmemBytes = M::kSmem;
-  cfg.stream = st;
+  cfg.dynamicSmemBytes = M::smem(true);
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
 
@@ -1205,67 +1303,77 @@ cudaError_t run(const DecodeArgs& p, cudaStream_t st) {
     const long long in_cluster = (most + size * M::kWarps - 1) / (size * M::kWarps);
     if (in_cluster > on_line + kClusterSlack) break;
     auto* kern = decode_kernel<D, M, true>;
-    cudaError_t e = allow_smem(kern, M::kSmem, ready_cluster);
+    cudaError_t e = allow_smem(kern, M::smem(true), ready_cluster);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(segs * size));
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = size;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    int at_once = 0;
     if (size > 1) {
+      int at_once = 0;
       e = clusters_at_once(kern, cfg, size, at_once, resident);
       if (e != cudaSuccess) return e;
       if (segs > at_once) continue;
     }
-    return cudaLaunchKernelEx(&cfg, kern, p, size, groups);
+    pl.size = size;
+    return cudaSuccess;
   }
-
-  const int units = p.kv_idx ? p.B * p.c.H : p.B;
   // never more CTAs than full tables give every warp a step
-  const int ctas = (int)std::min<long long>(p.sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
-  auto* kern = decode_kernel<D, M, false>;
-  cudaError_t e = allow_smem(kern, M::kSmem, ready_line);
-  if (e != cudaSuccess) return e;
-  kern<<<ctas, M::kThreads, M::kSmem, st>>>(p, units, groups);
+  pl.ctas = (int)std::min<long long>(p.sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
+  pl.bytes = (size_t)pl.ctas * (sizeof(Record) + (M::kWarps + 2) * (size_t)M::kRows * (D + 2) * 4);
+  return allow_smem(decode_kernel<D, M, false>, M::smem(false), ready_line);
+}
+
+// Runs the call, or only says how much scratch it takes (bytes).
+template <int D, class M>
+cudaError_t run(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  Plan pl;
+  cudaError_t e = plan<D, M>(p, cfg, attr, pl);
+  if (bytes) *bytes = pl.bytes;
+  if (bytes || e != cudaSuccess) return e;
+  cfg.stream = st;
+  if (pl.size) return cudaLaunchKernelEx(&cfg, decode_kernel<D, M, true>, p, pl.size, pl.groups);
+  decode_kernel<D, M, false><<<pl.ctas, M::kThreads, M::smem(false), st>>>(p, p.kv_idx ? p.B * p.c.H : p.B,
+                                                                    pl.groups);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // set up while the main kernel runs; it waits for that kernel's end before it reads
-  cfg.gridDim = dim3(ctas, (unsigned)std::min<long long>(R, M::kRows));
+  const long long R = (long long)(p.Hq / p.c.H) * p.T;
+  cfg.gridDim = dim3(pl.ctas, (unsigned)(std::min<long long>(R, M::kRows) + 3) / 4);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, M::kRows, M::kWarps>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, M::kRows, M::kWarps>, p, pl.ctas);
 }
 
 // The fewest rows per segment that hold the R rows of a kv head, up to 32 (more take further
 // segments, which read the keys again).
 template <int D, bool E4M3, bool TWO>
-cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st) {
+cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
   const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  if (R <= 8) return run<D, Math<D, E4M3, TWO, 1, 8, 3>>(p, st);
-  if (R <= 16) return run<D, Math<D, E4M3, TWO, 2, 8, 3>>(p, st);
-  return run<D, Math<D, E4M3, TWO, 4, 8, 2>>(p, st);
+  if (R <= 8) return run<D, Math<D, E4M3, TWO, 1, 12, 2>>(p, st, bytes);
+  if (R <= 16) return run<D, Math<D, E4M3, TWO, 2, 8, 3>>(p, st, bytes);
+  return run<D, Math<D, E4M3, TWO, 4, 8, 2>>(p, st, bytes);
+}
+
+cudaError_t run_type(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
+  const bool two = !p.c.e4m3 || p.out_dtype == SA_OUT_F32;
+  if (p.c.d == 64)
+    return !p.c.e4m3 ? run_rows<64, false, true>(p, st, bytes)
+           : two     ? run_rows<64, true, true>(p, st, bytes)
+                     : run_rows<64, true, false>(p, st, bytes);
+  return !p.c.e4m3 ? run_rows<128, false, true>(p, st, bytes)
+         : two     ? run_rows<128, true, true>(p, st, bytes)
+                   : run_rows<128, true, false>(p, st, bytes);
 }
 
 }  // namespace
 
-size_t decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms) {
-  if (B == 0 || Hq == 0) return 0;
-  const long long R = (long long)(Hq / Hkv) * T;
-  const int rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
-  return (size_t)sms * (sizeof(Record) + (kMaxWarps + 2) * (size_t)rows * (d + 2) * 4);
-}
+cudaError_t decode_work_bytes(const DecodeArgs& p, size_t* bytes) { return run_type(p, nullptr, bytes); }
 
-cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
-  const bool two = !p.c.e4m3 || p.out_dtype == SA_OUT_F32;
-  if (p.c.d == 64)
-    return !p.c.e4m3 ? run_rows<64, false, true>(p, st)
-           : two     ? run_rows<64, true, true>(p, st)
-                     : run_rows<64, true, false>(p, st);
-  return !p.c.e4m3 ? run_rows<128, false, true>(p, st)
-         : two     ? run_rows<128, true, true>(p, st)
-                   : run_rows<128, true, false>(p, st);
-}
+cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) { return run_type(p, st, nullptr); }
 
 }  // namespace sa

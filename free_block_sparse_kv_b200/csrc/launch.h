@@ -142,7 +142,7 @@ struct DecodeArgs {
 cudaError_t launch_cache_append(const CacheAppendArgs& p, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadArgs& p, cudaStream_t st);
 cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st);
-size_t decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms);
+cudaError_t decode_work_bytes(const DecodeArgs& p, size_t* bytes);
 
 // Byte offsets of launch_kmeans's work buffers in cwork and iwork, and the two ends.
 struct KmeansLayout {

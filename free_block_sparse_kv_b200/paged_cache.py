@@ -52,52 +52,64 @@ def allocate_cache(num_pages: int, H: int, page: int = 64, d: int = 128, dtype=t
 
 
 def _check_cache(c: PagedCache):
+    """(cache type, device, shape) of a well-formed pool."""
     k, v = c.k, c.v
-    if not (k.is_cuda and k.dim() == 4 and k.is_contiguous() and v.is_contiguous()
-            and v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
+    dt, dev, shape = k.dtype, k.device, k.shape
+    if not (k.is_cuda and len(shape) == 4 and k.is_contiguous() and v.is_contiguous()
+            and v.shape == shape and v.dtype == dt and v.device == dev):
         raise ValueError("a cache is two contiguous CUDA tensors [num_pages,H,page,d] of one type")
-    if k.dtype == torch.bfloat16:
+    if dt == torch.bfloat16:
         if c.k_scale is not None or c.v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        return C.SA_CACHE_BF16
-    if k.dtype != torch.float8_e4m3fn:
+        return C.SA_CACHE_BF16, dev, shape
+    if dt != torch.float8_e4m3fn:
         raise ValueError("a cache holds bfloat16 or float8_e4m3fn rows")
+    rows = shape[:3]
     for s in (c.k_scale, c.v_scale):
-        if s is None or s.dtype != torch.float8_e8m0fnu or s.shape != k.shape[:3] \
-                or not s.is_contiguous() or s.device != k.device:
+        if s is None or s.dtype != torch.float8_e8m0fnu or s.shape != rows \
+                or not s.is_contiguous() or s.device != dev:
             raise ValueError("an e4m3 cache needs contiguous float8_e8m0fnu scales [num_pages,H,page]")
-    return C.SA_CACHE_E4M3
+    return C.SA_CACHE_E4M3, dev, shape
 
 
 def _strides(name, x, shape, device):
     """Element strides (b, h, t) of bf16 rows; a dimension of one has stride 0."""
-    if x.dtype != torch.bfloat16 or x.device != device or tuple(x.shape) != tuple(shape):
+    if x.dtype != torch.bfloat16 or x.shape != shape or x.device != device:
         raise ValueError(f"{name} must be a bf16 tensor {tuple(shape)} on {device}")
-    st, sz = x.stride(), x.shape
-    if st[3] != 1 and x.numel():
+    sb, sh, st, sd = x.stride()
+    if sd != 1 and x.numel():
         raise ValueError(f"the rows of {name} must be contiguous")
-    return tuple(st[i] if sz[i] > 1 else 0 for i in range(3))
+    B, H, T, _ = shape
+    return sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0
 
 
 def _ints(name, x, shape, device):
-    if x.dtype != torch.int32 or x.device != device or tuple(x.shape) != tuple(shape) \
-            or not x.is_contiguous():
+    if x.dtype != torch.int32 or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}")
 
 
 def _table(x, B, device):
     """(width, stride) of a page table [B, width] whose rows are contiguous."""
-    if x.dtype != torch.int32 or x.device != device or x.dim() != 2 or x.shape[0] != B \
-            or (x.numel() and ((x.shape[1] > 1 and x.stride(1) != 1)
-                               or (B > 1 and x.stride(0) < x.shape[1]))):
-        raise ValueError(f"page_table must be an int32 tensor [{B}, width] on {device}")
-    return x.shape[1], x.stride(0) if x.numel() and B > 1 else x.shape[1]
+    shape = x.shape
+    if x.dtype == torch.int32 and len(shape) == 2 and shape[0] == B and x.device == device:
+        width = shape[1]
+        if B * width == 0:
+            return width, width
+        stride, step = x.stride()
+        if (width == 1 or step == 1) and (B == 1 or stride >= width):
+            return width, stride if B > 1 else width
+    raise ValueError(f"page_table must be an int32 tensor [{B}, width] on {device} with contiguous rows")
 
 
 def _flag(err_flag, device):
     if err_flag is not None and (err_flag.dtype != torch.int32 or err_flag.device != device
                                  or err_flag.numel() < 1):
         raise ValueError(f"err_flag must be an int32 tensor on {device}")
+
+
+# handle of a device's current stream (torch.cuda.current_stream builds a Stream around it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @contextlib.contextmanager
@@ -130,11 +142,11 @@ def cache_append(cache: PagedCache, k, v, page_table, start, count=None, err_fla
     """Write rows t < count[b] (all T when ``count`` is None) of k, v [B,H,T,d] at positions
     start[b] + t of sequence b. Rows may be strided (a token-major projection seen as
     [B,H,T,d]); an e4m3 cache quantises them on the way."""
-    dt = _check_cache(cache)
-    P, H, page, d = cache.k.shape
+    dt, dev, (P, H, page, d) = _check_cache(cache)
     if k.dim() != 4:
         raise ValueError("k must be [B,H,T,d]")
-    B, dev, shape = k.shape[0], cache.k.device, (k.shape[0], H, k.shape[2], d)
+    B, _, T, _ = k.shape
+    shape = (B, H, T, d)
     ks, vs = _strides("k", k, shape, dev), _strides("v", v, shape, dev)
     width, stride = _table(page_table, B, dev)
     _ints("start", start, (B,), dev)
@@ -142,19 +154,19 @@ def cache_append(cache: PagedCache, k, v, page_table, start, count=None, err_fla
         _ints("count", count, (B,), dev)
     _flag(err_flag, dev)
     with _on(dev, stream):
-        C.sparse_attn_cache_append(k, v, ks, vs, B, H, k.shape[2], d, page_table, width, stride,
+        C.sparse_attn_cache_append(k, v, ks, vs, B, H, T, d, page_table, width, stride,
                                    start, count, cache.k, cache.v, cache.k_scale, cache.v_scale,
-                                   dt, P, page, err_flag, None)
+                                   dt, P, page, err_flag, _raw_stream(dev.index))
 
 
 def cache_read(cache: PagedCache, page_table, lens, k, v, first=None, err_flag=None, stream=None):
     """Write rows first[b] <= t < lens[b] (from 0 when ``first`` is None) of every sequence
     to rows t of k, v [B,H,N,d] bf16; their other rows stay as they are."""
-    dt = _check_cache(cache)
-    P, H, page, d = cache.k.shape
+    dt, dev, (P, H, page, d) = _check_cache(cache)
     if k.dim() != 4:
         raise ValueError("k must be [B,H,N,d]")
-    B, dev, shape = k.shape[0], cache.k.device, (k.shape[0], H, k.shape[2], d)
+    B, _, N, _ = k.shape
+    shape = (B, H, N, d)
     ks, vs = _strides("k", k, shape, dev), _strides("v", v, shape, dev)
     _apart("k", k)
     _apart("v", v)
@@ -165,18 +177,14 @@ def cache_read(cache: PagedCache, page_table, lens, k, v, first=None, err_flag=N
     _flag(err_flag, dev)
     with _on(dev, stream):
         C.sparse_attn_cache_read(cache.k, cache.v, cache.k_scale, cache.v_scale, dt, P, page,
-                                 page_table, width, stride, first, lens, B, H, k.shape[2], d, k, v,
-                                 ks, vs, err_flag, None)
+                                 page_table, width, stride, first, lens, B, H, N, d, k, v,
+                                 ks, vs, err_flag, _raw_stream(dev.index))
 
 
 @functools.lru_cache(maxsize=1024)
-def _work_bytes(B, Hq, Hkv, T, d, sms):
-    return C.sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, sms)
-
-
-@functools.lru_cache(maxsize=64)
-def _sms(index):
-    return torch.cuda.get_device_properties(index).multi_processor_count
+def _work_bytes(device, *shape):
+    with torch.cuda.device(device):
+        return C.sparse_attn_decode_work_bytes(*shape)
 
 
 def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, scale=None,
@@ -191,12 +199,10 @@ def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, sca
     block = page, are taken as they are). A row that attends nothing is 0, its lse -inf.
     Returns ``out`` [B,Hq,T,d] (fp32, or bf16 by ``out_dtype``), and with ``return_lse`` also
     the fp32 log-sum-exp [B,Hq,T] of the scaled logits, by which partial results merge."""
-    dt = _check_cache(cache)
-    P, H, page, d = cache.k.shape
-    dev = cache.k.device
+    dt, dev, (P, H, page, d) = _check_cache(cache)
     if q.dim() != 4:
         raise ValueError("q must be [B,Hq,T,d]")
-    B, Hq, T = q.shape[0], q.shape[1], q.shape[2]
+    B, Hq, T, _ = q.shape
     qs = _strides("q", q, (B, Hq, T, d), dev)
     width, stride = _table(page_table, B, dev)
     _ints("lens", lens, (B,), dev)
@@ -220,14 +226,14 @@ def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, sca
         if out.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("the output is float32 or bfloat16")
         lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev) if return_lse else None
-        need = _work_bytes(B, Hq, H, T, d, _sms(dev.index))
+        odt = C.SA_OUT_F32 if out.dtype == torch.float32 else C.SA_OUT_BF16
+        need = _work_bytes(dev.index, B, Hq, H, T, d, dt, page, width, -1 if kv_idx is None else cap, odt)
         # scratch of this call alone: calls on other streams and captured graphs have their own
         work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         C.sparse_attn_decode(q, qs, B, Hq, H, T, d, cache.k, cache.v, cache.k_scale, cache.v_scale,
                              dt, P, page, page_table, width, stride, lens, kv_idx, kv_cnt, cap,
                              1.0 / math.sqrt(d) if scale is None else scale, work, out,
-                             C.SA_OUT_F32 if out.dtype == torch.float32 else C.SA_OUT_BF16, lse,
-                             err_flag, None)
+                             odt, lse, err_flag, _raw_stream(dev.index))
     return (out, lse) if return_lse else out
 
 

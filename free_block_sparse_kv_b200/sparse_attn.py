@@ -83,7 +83,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         [_P] * 2 + [_L] * 6 + [_P, _P]
     lib.sparse_attn_decode.argtypes = [_P] + [_L] * 3 + [_I] * 5 + [_P] * 4 + [_I] * 3 + \
         [_P, _I, _L] + [_P] * 3 + [_I, _F, _P, _P, _I, _P, _P, _P]
-    lib.sparse_attn_decode_work_bytes.argtypes = [_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.sparse_attn_decode_work_bytes.argtypes = [_I] * 10 + [ctypes.POINTER(ctypes.c_size_t)]
     for name in EXPORTS[:-1]:
         getattr(lib, name).restype = _I
     _lib = lib
@@ -91,9 +91,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     return x.data_ptr()
 
@@ -277,10 +275,13 @@ def sparse_attn_decode(q, q_strides, B, Hq, Hkv, T, d, k_pages, v_pages, k_scale
         _ptr(lse), _ptr(err_flag), _stream(stream)))
 
 
-def sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, sms=0) -> int:
-    """Scratch bytes of a decode on a device of ``sms`` SMs (0: the current device)."""
+def sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, cache_dtype, page, table_width, cap=-1,
+                                  out_dtype=SA_OUT_F32) -> int:
+    """Scratch bytes of a decode on the current device (``cap`` -1: no kept lists)."""
     out = ctypes.c_size_t(0)
-    _check(load_library().sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, sms, ctypes.byref(out)))
+    _check(load_library().sparse_attn_decode_work_bytes(B, Hq, Hkv, T, d, cache_dtype, page,
+                                                        table_width, cap, out_dtype,
+                                                        ctypes.byref(out)))
     return int(out.value)
 
 

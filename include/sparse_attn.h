@@ -485,9 +485,11 @@ int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_
                        const int32_t* kv_cnt, int cap, float scale, void* work, void* out,
                        int out_dtype, float* lse, int32_t* err_flag, void* stream);
 
-/* Bytes of `work` that sparse_attn_decode needs on a device of `sms` SMs (0: the current
- * device). They do not depend on the lengths or the table. Host only. */
-int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int sms, size_t* bytes);
+/* Bytes of `work` that sparse_attn_decode needs on the current device for a call of these
+ * sizes (cap -1: without lists): 0 where one cluster of CTAs takes each group of query rows.
+ * They do not depend on the lengths, the tables or the lists. Host only. */
+int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int cache_dtype, int page,
+                                  int table_width, int cap, int out_dtype, size_t* bytes);
 
 /* Message for the last error returned on the calling thread ("" if none). */
 const char* sparse_attn_last_error(void);

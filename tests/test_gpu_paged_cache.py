@@ -263,6 +263,13 @@ CASES = [  # B, Hq, H, T, d, page, lens
     (17, 2, 1, 1, 64, 256, list(range(0, 17 * 31, 31))),
     (1, 16, 16, 1, 128, 64, [1560]),
     (1, 4, 1, 3, 128, 16, [9001]),
+    # more sequences than a warp scans by itself, many of one step, some of none
+    (300, 2, 1, 1, 64, 16, [(7 * b) % 90 if b % 5 else 0 for b in range(300)]),
+    (600, 1, 1, 2, 128, 16, [1 + (b * b) % 37 for b in range(600)]),
+    # segments of one step and of many in turn, so that shares hold several and parts of others
+    (40, 16, 4, 1, 128, 16, [3 if b % 3 else 2000 for b in range(40)]),
+    (24, 36, 2, 1, 64, 32, [33 * b + 1 for b in range(24)]),
+    (5, 40, 1, 1, 128, 64, [4100, 1, 0, 2222, 640]),
 ]
 
 
@@ -319,6 +326,43 @@ def test_decode_kept_pages(B, Hq, H, T, d, page, lens, cap, dtype):
     out, lse = P.decode(q, c, _ints(table), _ints(lens), _ints(idx)[:, :, None],
                         _ints(cnt)[:, :, None], scale=-0.3, out_dtype=BF16, return_lse=True)
     _check(out, lse, BF16, d, -0.3, q, c, table, lens, page, full)
+
+
+def test_decode_kept_lists_of_many_heads():
+    """More (sequence, head) lists than a warp scans by itself."""
+    rng = np.random.default_rng(41)
+    B, H, d, page = 45, 8, 64, 16
+    lens = [(37 * b) % 150 for b in range(B)]
+    num = sum(-(-n // page) for n in lens) + 1
+    table = _table(rng, lens, page, num)
+    c = _filled(rng, num, H, page, d, E4M3)
+    q = _bf16(rng, B, 2 * H, 1, d)
+    kept = [[sorted(rng.choice(-(-n // page), rng.integers(0, -(-n // page) + 1), replace=False).tolist())
+             for _ in range(H)] for n in lens]
+    idx, cnt = np.zeros((B, H, 10), int), np.zeros((B, H), int)
+    for b in range(B):
+        for h in range(H):
+            idx[b, h, :len(kept[b][h])], cnt[b, h] = kept[b][h], len(kept[b][h])
+    out, lse = P.decode(q, c, _ints(table), _ints(lens), _ints(idx), _ints(cnt), return_lse=True)
+    _check(out, lse, F32, d, 1 / np.sqrt(d), q, c, table, lens, page, kept)
+
+
+def test_decode_zero_rows_beside_small_values():
+    """Rows of zeros (stored with scale 1) do not drown values of 1e-9 in 8 bits: the output
+    is compared on the values' own scale."""
+    rng = np.random.default_rng(43)
+    H, d, page, n = 2, 128, 32, 300
+    k, v = _bf16(rng, 1, H, n, d), _bf16(rng, 1, H, n, d, scale=1e-9)
+    v[:, :, ::3] = 0
+    v[:, 1, :, :] = 0          # and a head with nothing else
+    c = P.allocate_cache(10, H, page, d, E4M3)
+    table = [list(range(10))]
+    P.cache_append(c, k, v, _ints(table), _ints([0]))
+    q = _bf16(rng, 1, 4 * H, 1, d)
+    for dt in (F32, BF16):
+        out, lse = P.decode(q, c, _ints(table), _ints([n]), out_dtype=dt, return_lse=True)
+        _check(out, lse, dt, d, 1 / np.sqrt(d), q, c, table, [n], page)
+        assert not out[:, 4:].any() and out[:, :4].any()
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])

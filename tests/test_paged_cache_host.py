@@ -120,10 +120,13 @@ def test_refusals(lib):
         with pytest.raises(C.SparseAttnError) as e:
             fn(**kw)
         assert e.value.code == C.SA_ERR_INVALID, (fn.__name__, kw, str(e.value))
-    for kw in (dict(T=0), dict(d=80), dict(Hq=3, H=2)):
-        a = dict(B=1, Hq=2, H=1, T=1, d=128) | kw
-        with pytest.raises(C.SparseAttnError):
-            C.sparse_attn_decode_work_bytes(a["B"], a["Hq"], a["H"], a["T"], a["d"], 148)
+    for kw in (dict(T=0), dict(d=80), dict(Hq=3, Hkv=2), dict(dt=2), dict(page=24), dict(width=-1),
+               dict(width=1 << 28), dict(cap=-2), dict(cap=1 << 28), dict(odt=3)):
+        a = dict(B=1, Hq=2, Hkv=1, T=1, d=128, dt=1, page=16, width=4, cap=-1, odt=0) | kw
+        with pytest.raises(C.SparseAttnError) as e:
+            C.sparse_attn_decode_work_bytes(*a.values())
+        assert e.value.code == C.SA_ERR_INVALID
+    assert C.sparse_attn_decode_work_bytes(0, 2, 1, 1, 128, 1, 16, 4) == 0
     # empty calls look at no buffer
     app(B=0, k=None, v=None, kp=None, table=None, start=None)
     app(T=0, k=None, v=None, kp=None, table=None, start=None)
