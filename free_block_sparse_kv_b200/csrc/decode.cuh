@@ -3,9 +3,9 @@
 // Per (b, kv head h) the R = (Hq / Hkv) * T query rows (g, t) that share the head's keys:
 //   l_p = scale * q . k_p over the positions p < len - (T - 1 - t) of the listed pages,
 //   o = sum e^(l_p - m) v_p / sum e^(l_p - m),   lse = m + ln sum e^(l_p - m),
-// in one pass over K and V with a running maximum m and sum in fp32 (base 2). Every cached
+// in one pass over K and V with a running level m and a sum in fp32 (base 2). Every cached
 // row is read once for all R rows, at 4 R d operations per 4 d (bf16) or 2 d + 2 (e4m3)
-// bytes: HBM bounds it up to R of about 32, so the design is about keeping loads in flight
+// bytes: HBM bounds it up to R of about 16, so the design is about keeping loads in flight
 // and every SM equally loaded:
 //  - The work is cut into steps of 4 KB of K and 4 KB of V (16 to 64 keys). All steps of all
 //    (sequence, kv head, group of rows) segments form one line, in which every warp of a
@@ -13,19 +13,31 @@
 //    are found on the device from the lengths (a scan of one weight per sequence), so a
 //    captured graph follows the lengths.
 //  - A warp streams its steps through its own ring of cp.async stages, 16 bytes a lane, with
-//    no barrier between warps; it looks page numbers up one step ahead.
+//    no barrier between warps. Page numbers are looked up for up to 32 steps at a time, one
+//    step ahead (a look-up at the copy it serves left the warp waiting 600 cycles a step).
 //  - A segment that ends inside the share it began in is written out at once; the others
 //    leave (m, l, numerator) partials, joined first inside the CTA and then, for segments
 //    that span CTAs, by a second small kernel. Orders are fixed: same bits every run.
+//  - Where one cluster per segment fills the GPU about as well (few, short segments), that
+//    takes one launch and no scan: 16 heads of 1,560 rows 10.4 us against 16.5 on the line.
 //  - Products run on mma.sync with the keys as the M dimension (S^T = K Q^T, O^T = V^T P^T):
-//    one query row wastes 7/8 of a tile, not 15/16, and the tensor work stays far below the
-//    time of the loads. Larger tensor instructions would leave the bound where it is.
-// Roundings below fp32: P enters its product as two 16-bit pieces (high and rest, 2^-17 of
-// each weight for bf16, 2^-23 for f16), because one bf16 piece (2^-9) would show in an fp32
-// output. e4m3 codes enter as f16, exactly; the query then enters as f16 times a power of
-// two per row that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that
-// value). The scale of a V row is folded into its weight: numerator weights carry their own
-// running maximum of l_p + log2(scale_p), so that no scale can overflow or starve them.
+//    one query row wastes 7/8 of a tile, not 15/16, and the tensor work (2 cycles of an SM a
+//    product) stays below the time of the loads up to R = 16. At R = 32 it is about half of
+//    what bounds the kernel; a tile of 128 keys on the larger tensor instructions is what
+//    would move that.
+//  - Twelve warps of two stages where eight rows suffice, eight of three or two otherwise
+//    (registers): 64 ragged e4m3 sequences 108 us against 121 with eight warps of three.
+// Measured on one B200 (device time, calls back to back): 4 x 16 heads x 63,960 bf16 rows
+// 314 us (6.67 TB/s); 40 heads x 75,600 e4m3 rows 131 us (5.9 TB/s); 64 e4m3 sequences of 0
+// to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 103 us (5.3 TB/s).
+//
+// Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
+// before: as many as keep the dropped rest below the output's own rounding (run_decode()).
+// e4m3 codes enter as f16, exactly; the query then enters as f16 times a power of two per row
+// that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that value). The
+// scale of a V row is folded into its weight: numerator weights carry their own level, the
+// running maximum of l_p + log2(scale_p), so that no scale can overflow or starve them. The
+// levels follow the maxima when those outgrow them by 2^4, so a weight is at most 2^4.
 #pragma once
 
 #include <algorithm>
@@ -37,9 +49,11 @@
 namespace sa {
 namespace {
 
-constexpr int kLaneUnits = 8;
+constexpr int kLaneUnits = 8;          // units of a lane where a warp scans them by itself
 // A cluster per segment saves the scan, the partials' way through memory and the second
-// kernel, about as long as this many steps of a warp take.
+// kernel: 5 us, about as long as this many steps of a warp take (1.3 us each when all SMs
+// load). With 100 kept pages of 64 rows in each of 64 heads (10 steps in clusters of two, 8
+// on the line) it takes 41 us against 50.
 constexpr long long kClusterSlack = 4;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 // The level that a column's weights are relative to follows its running maximum only when that
@@ -118,6 +132,7 @@ SA_DEVI void ldsm_t8(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
+
 // What a step's tiles are and where: shared-memory addresses of its K and V rows, scales
 // and tile positions, and the segment's length.
 struct Step {
@@ -1383,8 +1398,9 @@ cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
 }  // namespace
 
 // Pieces of a weight: as many as keep what they drop below the output's own rounding (half a
-// step, 2^-9 of a bf16 value): one f16 piece drops 2^-12, two bf16 pieces 2^-17; for fp32
-// outputs two f16 pieces drop 2^-23 and three bf16 pieces 2^-25.
+// step: 2^-8 of a bf16 value at most, 2^-24 of fp32): one f16 piece drops 2^-11 of a weight
+// at most and two bf16 pieces 2^-16; for fp32 outputs two f16 pieces drop 2^-22 and three
+// bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds.
 template <int D>
 cudaError_t run_decode(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
   const bool f32 = p.out_dtype == SA_OUT_F32;

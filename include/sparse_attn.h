@@ -464,7 +464,8 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  *   l_p = scale * q . k_p,  o = sum_p e^(l_p) v_p / sum_p e^(l_p),  lse = ln sum_p e^(l_p)
  * A row that attends nothing (an empty sequence, an empty list, t < T - lens[b]) gets
  * o = 0 and lse = -inf. A position that a row does not attend never reaches it, whatever
- * its K and V hold; an attended non-finite K or V gives a non-finite output.
+ * its K and V hold; infinities and NaN that it attends act as in the formulas, but an
+ * infinity of V may come out as NaN.
  *   q        [B,Hq,T,d] bf16 (strided), 1 <= T <= 16; Hq a multiple of Hkv
  *   kv_idx   [B,Hkv,cap] int32 and kv_cnt [B,Hkv]: kept logical pages of each kv head in
  *            the list format of routing (the lists of one query block, block = page;
@@ -474,8 +475,11 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  *            bytes for the current device (may be NULL when that is 0). Its contents need
  *            no initialisation; calls that may run at the same time need one each
  *   out      [B,Hq,T,d] contiguous, fp32 or bf16;  lse [B,Hq,T] fp32 or NULL
- * Logits, maxima, sums and accumulators are fp32. The result is the same bit for bit from
- * run to run on one kind of device.
+ * Logits, maxima, sums and accumulators are fp32; the weights enter their product with V in
+ * 16-bit pieces that together keep 2^-11 (e4m3) or 2^-16 (bf16) of each for a bf16 output and
+ * 2^-22 or better for fp32. The result is the same bit for bit from run to run on one kind of
+ * device. One launch (one thread-block cluster per group of query rows) for few and short
+ * sequences, otherwise two (the second joins what CTAs share).
  */
 int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
                        int Hkv, int T, int d, const void* k_pages, const void* v_pages,
