@@ -13,17 +13,22 @@ namespace sa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;      // rows of K and of V in flight per thread, append
-constexpr int kReadUnroll = 4;  // and read
+constexpr int kAppendUnroll = 2;  // rows of K and of V in flight per thread, append
+constexpr int kReadUnroll = 4;    // and read
 constexpr int kReadBlocks = 148 * 16;   // blocks of a read that has work for them
+
+SA_DEVI uint32_t max_abs2(uint32_t a, uint32_t b) {   // of bf16 pairs; NaN stays NaN
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 // The row's largest magnitude as bf16 bits, over the LPR lanes that share the row.
 template <int LPR>
 SA_DEVI uint32_t row_top(const uint4& x) {
-  uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                          __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  uint32_t top = max_abs2(max_abs2(x.x, x.y), max_abs2(x.z, x.w));
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+  for (int o = LPR / 2; o > 0; o >>= 1) top = max_abs2(top, __shfl_xor_sync(~0u, top, o));
   return max(top & 0xFFFFu, top >> 16);
 }
 
@@ -52,15 +57,19 @@ SA_DEVI uint32_t row_scale(uint32_t top) {
   return (uint32_t)max(e, 1);
 }
 
-// Four bf16 pairs * 2^(127 - s) -> eight e4m3 codes.
+// Four bf16 pairs * 2^(127 - s) -> eight e4m3 codes. The product is exact in bf16 (what would
+// fall below bf16's smallest normal value is far below e4m3's).
 SA_DEVI uint2 row_codes(const uint4& x, uint32_t s) {
-  const float inv = __uint_as_float((254u - s) << 23);
+  const uint32_t inv = (254u - s) * 0x00800080u;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv),
-                                    __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&inv));
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(v), bf16_hi(v)), __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
@@ -76,10 +85,12 @@ SA_DEVI uint2 quantise(uint4 x, uint32_t& s) {
   return row_codes(x, s);
 }
 
-template <int D, bool E4M3>
+// A block takes RPP * UNROLL rows: of one head's tokens, or (FLAT: few tokens) of all heads' in
+// (head, token) order.
+template <int D, bool E4M3, bool FLAT>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendArgs p) {
-  constexpr int LPR = D / 8, RPP = kThreads / LPR;
-  const int b = blockIdx.y;
+  constexpr int LPR = D / 8, RPP = kThreads / LPR, UNROLL = FLAT ? 1 : kAppendUnroll;
+  const int b = FLAT ? blockIdx.y : blockIdx.z;
   const int start = p.start[b];
   int n = p.count ? p.count[b] : p.T;
   if (n < 0 || n > p.T || start < 0) {
@@ -87,33 +98,42 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendArgs 
       atomicOr(p.c.err_flag, SA_FLAG_INDEX_BIT);
     n = start < 0 || n < 0 ? 0 : p.T;
   }
-  const int page = 1 << p.c.page_log2, lane = threadIdx.x % LPR;
-  const long long rows = (long long)p.c.H * p.T;
-  const long long r0 = (long long)blockIdx.x * (RPP * kUnroll) + threadIdx.x / LPR;
-  uint4 kx[kUnroll], vx[kUnroll];
-  int64_t dst[kUnroll];
+  const int in_page = (1 << p.c.page_log2) - 1, lane = threadIdx.x % LPR;
+  const uint32_t r0 = blockIdx.x * (RPP * UNROLL) + threadIdx.x / LPR;
+  uint32_t h = FLAT ? r0 / (uint32_t)p.T : blockIdx.y, t0 = FLAT ? r0 - h * (uint32_t)p.T : r0;
+  if (FLAT && h >= (uint32_t)p.c.H) {
+    h = 0;
+    t0 = (uint32_t)p.T;
+  }
+  const uint16_t* kp = p.k + b * p.ks.b + h * p.ks.h + lane * 8;
+  const uint16_t* vp = p.v + b * p.vs.b + h * p.vs.h + lane * 8;
+  const int32_t* table = p.c.table + b * p.c.table_stride;
+  uint4 kx[UNROLL], vx[UNROLL];
+  int64_t dst[UNROLL];      // row of the pool, -1: none
+  int pg[UNROLL];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long r = r0 + u * RPP;
-    dst[u] = -1;
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t t = t0 + u * RPP;
+    pg[u] = -1;
     kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-    if (r >= rows) continue;
-    const int h = (int)((uint32_t)r / (uint32_t)p.T), t = (int)((uint32_t)r % (uint32_t)p.T);
-    if (t >= n) continue;
-    const int64_t pos = (int64_t)start + t;
-    const int64_t lp = pos >> p.c.page_log2;
-    if (lp >= p.c.table_width) {
-      if (p.c.err_flag) atomicOr(p.c.err_flag, SA_FLAG_INDEX_BIT);
-      continue;
+    if (t < (uint32_t)n) {
+      const uint32_t lp = ((uint32_t)start + t) >> p.c.page_log2;     // both below 2^31
+      if (lp < (uint32_t)p.c.table_width) pg[u] = table[lp];
+      kx[u] = __ldg(reinterpret_cast<const uint4*>(kp + t * p.ks.t));
+      vx[u] = __ldg(reinterpret_cast<const uint4*>(vp + t * p.vs.t));
     }
-    const int pg = pool_page(p.c, b, (int)lp);
-    if (pg < 0) continue;
-    dst[u] = (((int64_t)pg * p.c.H + h) << p.c.page_log2) + (pos & (page - 1));
-    kx[u] = __ldg(reinterpret_cast<const uint4*>(p.k + b * p.ks.b + h * p.ks.h + t * p.ks.t) + lane);
-    vx[u] = __ldg(reinterpret_cast<const uint4*>(p.v + b * p.vs.b + h * p.vs.h + t * p.vs.t) + lane);
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t t = t0 + u * RPP;
+    dst[u] = -1;
+    if ((unsigned)pg[u] < (unsigned)p.c.num_pages)
+      dst[u] = (((int64_t)pg[u] * p.c.H + h) << p.c.page_log2) + (((uint32_t)start + t) & in_page);
+    else if (t < (uint32_t)n && p.c.err_flag)
+      atomicOr(p.c.err_flag, SA_FLAG_INDEX_BIT);
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
     if constexpr (E4M3) {
       uint32_t ks, vs;
       const uint2 kc = quantise<LPR>(kx[u], ks), vc = quantise<LPR>(vx[u], vs);
@@ -199,12 +219,18 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadArgs p) {
   }
 }
 
+// A head's tokens fill a block's rows, or the rows of all heads are dealt out in one.
 template <int D, bool E4M3>
 cudaError_t append_t(const CacheAppendArgs& p, cudaStream_t st) {
-  constexpr int per = kThreads / (D / 8) * kUnroll;
-  const long long rows = (long long)p.c.H * p.T;
-  const dim3 grid((unsigned)((rows + per - 1) / per), (unsigned)p.B);
-  cache_append_kernel<D, E4M3><<<grid, kThreads, 0, st>>>(p);
+  constexpr int rpp = kThreads / (D / 8);
+  if (p.T >= rpp * kAppendUnroll) {
+    const dim3 grid((unsigned)(((long long)p.T + rpp * kAppendUnroll - 1) / (rpp * kAppendUnroll)),
+                    (unsigned)p.c.H, (unsigned)p.B);
+    cache_append_kernel<D, E4M3, false><<<grid, kThreads, 0, st>>>(p);
+  } else {
+    const dim3 grid((unsigned)(((long long)p.c.H * p.T + rpp - 1) / rpp), (unsigned)p.B);
+    cache_append_kernel<D, E4M3, true><<<grid, kThreads, 0, st>>>(p);
+  }
   return cudaGetLastError();
 }
 
