@@ -555,6 +555,41 @@ def test_append_and_read_in_a_graph_on_a_stream():
                 assert np.array_equal(_np(got)[b, :, s + step], code * sc[:, None])
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("B,Hq,H,T,d,page,lens", [
+    (2, 3, 1, 1, 64, 16, [1, 77]), (1, 8, 8, 5, 128, 64, [129]), (3, 40, 2, 2, 128, 16, [0, 31, 333]),
+    (40, 16, 4, 1, 128, 16, [3 if b % 3 else 2000 for b in range(40)])])
+def test_every_write_stays_in_its_buffer(B, Hq, H, T, d, page, lens, dtype):
+    """Pools, outputs and scratch (of exactly the stated size) between canary regions."""
+    from tests.test_gpu_canary import Guarded
+    rng = np.random.default_rng(B + T)
+    num = sum(-(-n // page) for n in lens) + 1
+    table = _table(rng, lens, page, num)
+    tab, ln = _ints(table), _ints(lens)
+    g = dict(k=Guarded((num, H, page, d), dtype), v=Guarded((num, H, page, d), dtype))
+    if dtype == E4M3:
+        g.update(ks=Guarded((num, H, page), torch.float8_e8m0fnu), vs=Guarded((num, H, page), torch.float8_e8m0fnu))
+    c = P.PagedCache(g["k"].t, g["v"].t, *(g[n].t for n in ("ks", "vs") if n in g))
+    N = max(lens)
+    k, v = _bf16(rng, B, H, N, d), _bf16(rng, B, H, N, d)
+    P.cache_append(c, k, v, tab, _ints([0] * B), ln)
+    g.update(k_out=Guarded((B, H, N, d), BF16), v_out=Guarded((B, H, N, d), BF16))
+    P.cache_read(c, tab, ln, g["k_out"].t, g["v_out"].t)
+    q = _bf16(rng, B, Hq, T, d)
+    for odt, code in ((F32, C.SA_OUT_F32), (BF16, C.SA_OUT_BF16)):
+        dt = C.SA_CACHE_BF16 if dtype == BF16 else C.SA_CACHE_E4M3
+        need = C.sparse_attn_decode_work_bytes(B, Hq, H, T, d, dt, page, table.shape[1], -1, code)
+        g.update(work=Guarded((need,), torch.uint8), out=Guarded((B, Hq, T, d), odt),
+                 lse=Guarded((B, Hq, T), F32))
+        C.sparse_attn_decode(q, q.stride()[:3], B, Hq, H, T, d, c.k, c.v, c.k_scale, c.v_scale, dt, num,
+                             page, tab, table.shape[1], table.shape[1], ln, None, None, 0, d ** -0.5,
+                             g["work"].t if need else None, g["out"].t, code, g["lse"].t)
+        torch.cuda.synchronize()
+        for name, x in g.items():
+            assert x.intact(), name
+        _check(g["out"].t, g["lse"].t, odt, d, 1 / np.sqrt(d), q, c, table, lens, page)
+
+
 def test_python_checks():
     c = P.allocate_cache(4, 2, 16, 64, E4M3)
     q = torch.zeros(1, 4, 1, 64, dtype=BF16, device="cuda")
