@@ -9,7 +9,7 @@
 // and every SM equally loaded:
 //  - The work is cut into steps of 4 KB of K and 4 KB of V (16 to 64 keys). All steps of all
 //    (sequence, kv head, group of rows) segments form one line, in which every warp of a
-//    grid of one CTA per SM takes an equal, contiguous share, whatever the lengths. Shares
+//    grid of at most one CTA per SM takes an equal, contiguous share, whatever the lengths. Shares
 //    are found on the device from the lengths (a scan of one weight per sequence), so a
 //    captured graph follows the lengths.
 //  - A warp streams its steps through its own ring of cp.async stages, 16 bytes a lane, with
@@ -27,9 +27,9 @@
 //    would move that.
 //  - Twelve warps of two stages where eight rows suffice, eight of three or two otherwise
 //    (registers): 64 ragged e4m3 sequences 108 us against 121 with eight warps of three.
-// Measured on one B200 (device time, calls back to back): 4 x 16 heads x 63,960 bf16 rows
-// 314 us (6.67 TB/s); 40 heads x 75,600 e4m3 rows 131 us (5.9 TB/s); 64 e4m3 sequences of 0
-// to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 103 us (5.3 TB/s).
+// Measured on one B200 (calls back to back, inputs of three in turn): 4 x 16 heads x 63,960
+// bf16 rows 304-325 us (6.9-6.4 TB/s); 40 heads x 75,600 e4m3 rows 131 us (5.9 TB/s); 64 e4m3
+// sequences of 0 to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 106 us (5.2 TB/s).
 //
 // Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
 // before: as many as keep the dropped rest below the output's own rounding (run_decode()).
@@ -52,8 +52,10 @@ namespace {
 constexpr int kLaneUnits = 8;          // units of a lane where a warp scans them by itself
 // A cluster per segment saves the scan, the partials' way through memory and the second
 // kernel: 5 us, about as long as this many steps of a warp take (1.3 us each when all SMs
-// load). With 100 kept pages of 64 rows in each of 64 heads (10 steps in clusters of two, 8
-// on the line) it takes 41 us against 50.
+// load). With 100 kept pages of 64 rows in each of 64 heads (17 steps in clusters of two, 15
+// on the line) it takes 40 us against 45. Longer ones run on the line, which their lengths
+// cannot unbalance (64 heads of 100 to 32,000 rows: 84 us against 95), but for one sequence
+// alone: 16 heads x 32,000 rows 48 us in clusters of four, 51 on the line.
 constexpr long long kClusterSlack = 4;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 // The level that a column's weights are relative to follows its running maximum only when that
@@ -1369,7 +1371,11 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   const long long on_line = (segs * most + (long long)p.sms * M::kWarps - 1) / ((long long)p.sms * M::kWarps);
   for (; size >= 1 && segs * size <= p.sms; size /= 2) {
     const long long in_cluster = (most + size * M::kWarps - 1) / (size * M::kWarps);
-    if (in_cluster > on_line + kClusterSlack) break;
+    // one sequence's heads are equally long, and 64 SMs come close to what HBM gives bf16 rows
+    // of up to eight queries; 8-bit rows and more queries need the SMs' own rate
+    const bool even = p.B == 1 && !p.kv_idx &&
+                      segs * size * (M::kE4M3 || M::kRows > 8 ? 12 : 24) >= 10ll * p.sms;
+    if (in_cluster > on_line + kClusterSlack && !even) break;
     auto* kern = decode_kernel<D, M, true>;
     cudaError_t e = allow_smem(kern, M::smem(true), ready_cluster);
     if (e != cudaSuccess) return e;
@@ -1386,8 +1392,14 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
     pl.size = size;
     return cudaSuccess;
   }
-  // never more CTAs than full tables give every warp a step
-  pl.ctas = (int)std::min<long long>(p.sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
+  // Up to eight query rows HBM is the bound, and eight SMs in nine ask for as much as it gives;
+  // 132 CTAs against 148, inputs of three calls in turn: 4 x 16 heads x 63,960 bf16 rows 304 us
+  // against 320 (on another B200 325 against 321), 40 heads x 75,600 e4m3 rows 131 against 134,
+  // 64 ragged e4m3 sequences 106 against 104. More rows need every SM (32 rows a segment, 8 x 8
+  // heads x 16,000: 116 against 112). And never more CTAs than full tables give every warp a
+  // step.
+  const int sms = M::kRows <= 8 ? p.sms - p.sms / 9 : p.sms;
+  pl.ctas = (int)std::min<long long>(sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
   pl.bytes = (size_t)pl.ctas * (sizeof(Record) + (M::kWarps + 2) * (size_t)M::kRows * (D + 2) * 4);
   return allow_smem(decode_kernel<D, M, false>, M::smem(false), ready_line);
 }
