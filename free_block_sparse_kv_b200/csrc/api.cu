@@ -690,10 +690,10 @@ int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_
   if (int rc = sm_count(&sms)) return rc;
   sa::DecodeArgs p{c, q, qs, B, Hq, T, lens, kv_idx, kv_cnt, cap, scale, sms, work, out, out_dtype,
                    lse};
-  size_t need = 0;
-  if (cudaError_t e = sa::decode_work_bytes(p, &need)) return launched(e, "decode plan");
-  if (need) SA_REQUIRE_PTR(work);
-  return launched(sa::launch_decode(p, static_cast<cudaStream_t>(stream)), "decode launch");
+  bool no_work = false;      // the call needs scratch and has none: nothing was enqueued
+  const cudaError_t e = sa::launch_decode(p, static_cast<cudaStream_t>(stream), &no_work);
+  if (no_work) SA_REQUIRE_PTR(work);
+  return launched(e, "decode launch");
 }
 
 int sparse_attn_decode_work_bytes(int B, int Hq, int Hkv, int T, int d, int cache_dtype, int page,

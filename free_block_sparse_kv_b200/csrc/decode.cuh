@@ -1406,13 +1406,17 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
 
 // Runs the call, or only says how much scratch it takes (bytes).
 template <int D, class M>
-cudaError_t run(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
+cudaError_t run(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_work) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   Plan pl;
   cudaError_t e = plan<D, M>(p, cfg, attr, pl);
   if (bytes) *bytes = pl.bytes;
   if (bytes || e != cudaSuccess) return e;
+  if (pl.bytes && (!p.work || (reinterpret_cast<uintptr_t>(p.work) & 15u))) {
+    *no_work = true;
+    return cudaSuccess;
+  }
   cfg.stream = st;
   if (pl.size) return cudaLaunchKernelEx(&cfg, decode_kernel<D, M, true>, p, pl.size, pl.groups);
   decode_kernel<D, M, false><<<pl.ctas, M::kThreads, M::smem(false), st>>>(p, p.kv_idx ? p.B * p.c.H : p.B,
@@ -1432,11 +1436,11 @@ cudaError_t run(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
 // The fewest rows per segment that hold the R rows of a kv head, up to 32 (more take further
 // segments, which read the keys again).
 template <int D, bool E4M3, int PIECES>
-cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
+cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_work) {
   const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  if (R <= 8) return run<D, Math<D, E4M3, PIECES, 1, 12, 2>>(p, st, bytes);
-  if (R <= 16) return run<D, Math<D, E4M3, PIECES, 2, 8, 3>>(p, st, bytes);
-  return run<D, Math<D, E4M3, PIECES, 4, 8, 2>>(p, st, bytes);
+  if (R <= 8) return run<D, Math<D, E4M3, PIECES, 1, 12, 2>>(p, st, bytes, no_work);
+  if (R <= 16) return run<D, Math<D, E4M3, PIECES, 2, 8, 3>>(p, st, bytes, no_work);
+  return run<D, Math<D, E4M3, PIECES, 4, 8, 2>>(p, st, bytes, no_work);
 }
 
 }  // namespace
@@ -1446,10 +1450,11 @@ cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
 // at most and two bf16 pieces 2^-16; for fp32 outputs two f16 pieces drop 2^-22 and three
 // bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds.
 template <int D>
-cudaError_t run_decode(const DecodeArgs& p, cudaStream_t st, size_t* bytes) {
+cudaError_t run_decode(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_work) {
   const bool f32 = p.out_dtype == SA_OUT_F32;
-  if (p.c.e4m3) return f32 ? run_rows<D, true, 2>(p, st, bytes) : run_rows<D, true, 1>(p, st, bytes);
-  return f32 ? run_rows<D, false, 3>(p, st, bytes) : run_rows<D, false, 2>(p, st, bytes);
+  if (p.c.e4m3)
+    return f32 ? run_rows<D, true, 2>(p, st, bytes, no_work) : run_rows<D, true, 1>(p, st, bytes, no_work);
+  return f32 ? run_rows<D, false, 3>(p, st, bytes, no_work) : run_rows<D, false, 2>(p, st, bytes, no_work);
 }
 
 }  // namespace sa

@@ -141,7 +141,8 @@ struct DecodeArgs {
 
 cudaError_t launch_cache_append(const CacheAppendArgs& p, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadArgs& p, cudaStream_t st);
-cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st);
+// *no_work: the call needs scratch and p.work is null or not 16-byte aligned; nothing was enqueued.
+cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st, bool* no_work);
 cudaError_t decode_work_bytes(const DecodeArgs& p, size_t* bytes);
 
 // Byte offsets of launch_kmeans's work buffers in cwork and iwork, and the two ends.

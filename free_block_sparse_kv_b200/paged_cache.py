@@ -114,18 +114,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 @contextlib.contextmanager
 def _guard(device, stream):
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(device, stream):
     """Context that makes ``device`` and ``stream`` current (nothing where they are)."""
     if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return _HERE
     return _guard(device, stream)
 
 
