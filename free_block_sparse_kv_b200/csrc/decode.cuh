@@ -19,7 +19,7 @@
 //    leave (m, l, numerator) partials, joined first inside the CTA and then, for segments
 //    that span CTAs, by a second small kernel. Orders are fixed: same bits every run.
 //  - Where one cluster per segment fills the GPU about as well (few, short segments), that
-//    takes one launch and no scan: 16 heads of 1,560 rows 10.4 us against 16.5 on the line.
+//    takes one launch and no scan: 16 heads of 1,560 rows 10.4 us against 12.4 on the line.
 //  - Products run on mma.sync with the keys as the M dimension (S^T = K Q^T, O^T = V^T P^T):
 //    one query row wastes 7/8 of a tile, not 15/16, and the tensor work (2 cycles of an SM a
 //    product) stays below the time of the loads up to R = 16. At R = 32 it is about half of
