@@ -27,9 +27,10 @@
 //    would move that.
 //  - Twelve warps of two stages where eight rows suffice, eight of three or two otherwise
 //    (registers): 64 ragged e4m3 sequences 108 us against 121 with eight warps of three.
-// Measured on one B200 (calls back to back, inputs of three in turn): 4 x 16 heads x 63,960
-// bf16 rows 304-325 us (6.9-6.4 TB/s); 40 heads x 75,600 e4m3 rows 131 us (5.9 TB/s); 64 e4m3
-// sequences of 0 to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 106 us (5.2 TB/s).
+// Measured on three B200s (calls back to back, inputs of three in turn): 4 x 16 heads x 63,960
+// bf16 rows 298-325 us (7.0-6.4 TB/s); 40 heads x 75,600 e4m3 rows 126-132 us (6.2-5.9 TB/s);
+// 64 e4m3 sequences of 0 to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 101-106 us
+// (5.4-5.2 TB/s).
 //
 // Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
 // before: as many as keep the dropped rest below the output's own rounding (run_decode()).
