@@ -640,8 +640,18 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
       for (int k = 0; k < 2; ++k) {
         l[nt][k] = col_sum(l[nt][k]);
         float x = 1.f;
-        if constexpr (E4M3)
-          x = mv[nt][k] == -INFINITY ? 0.f : ex2a(mv[nt][k] - kShift16 - ref_of(m[nt][k]));
+        if constexpr (E4M3) {
+          // 2^(mv - shift - m) as two factors: for V rows near the smallest scale (2^-126) the
+          // one would be flushed to zero, though the values are not
+          const float e = mv[nt][k] == -INFINITY ? -INFINITY : mv[nt][k] - kShift16 - ref_of(m[nt][k]);
+          const float a = ex2a(0.5f * e);
+          x = a;
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) {
+            o[mt][nt][k] *= a;
+            o[mt][nt][k + 2] *= a;
+          }
+        }
         if (whole) x = l[nt][k] == 0.f ? 0.f : x / l[nt][k];
         f[nt][k] = x;
       }

@@ -1,0 +1,47 @@
+"""Decode over a paged cache where numbers are hard: values of very different sizes, long sums,
+logits far from zero. Each tolerance is derived where it is used (u = 2^-24)."""
+import numpy as np
+import pytest
+import torch
+
+from free_block_sparse_kv_b200 import paged_cache as P
+from free_block_sparse_kv_b200 import sparse_attn as C
+from oracle import paged_cache as O
+from tests.test_gpu_paged_cache import BF16, E4M3, F32, _bf16, _bounds, _check, _ints, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    C.load_library()
+
+
+def _cache(k, v, page, dtype):
+    """The rows k, v [1,H,n,d] in the pages of one sequence, and its table."""
+    _, H, n, d = k.shape
+    num = -(-n // page)
+    c = P.allocate_cache(num, H, page, d, dtype)
+    table = [list(range(num))[::-1]]
+    P.cache_append(c, k, v, _ints(table), _ints([0]))
+    return c, table
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("n,page", [(40, 16), (3000, 64)])
+def test_values_near_the_smallest(n, page, out_dtype):
+    """Values of 2^-112 and 2^-118 (8-bit rows hold them with scales down to 2^-126) are
+    attended like any others: compared on their own scale. What fp32 itself drops there is
+    2^-149, 2^-31 of the smaller ones."""
+    rng = np.random.default_rng(n)
+    H, d = 2, 128
+    k, v = _bf16(rng, 1, H, n, d), _bf16(rng, 1, H, n, d)
+    v = (v.float() * torch.tensor([2.0 ** -112, 2.0 ** -118], device="cuda").view(1, 2, 1, 1)).to(BF16)
+    q = _bf16(rng, 1, 2 * H, 1, d)
+    for dtype in (E4M3, BF16):
+        c, table = _cache(k, v, page, dtype)
+        out, lse = P.decode(q, c, _ints(table), _ints([n]), out_dtype=out_dtype, return_lse=True)
+        _check(out, lse, out_dtype, d, 1 / np.sqrt(d), q, c, table, [n], page)
+        assert out.any(-1).all()
