@@ -37,8 +37,9 @@
 // e4m3 codes enter as f16, exactly; the query then enters as f16 times a power of two per row
 // that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that value). The
 // scale of a V row is folded into its weight: numerator weights carry their own level, the
-// running maximum of l_p + log2(scale_p), so that no scale can overflow or starve them. The
-// levels follow the maxima when those outgrow them by 2^4, so a weight is at most 2^4.
+// running maximum of l_p + log2(scale_p), so that no scale can overflow or starve them. A level
+// that a running maximum passes is set 2^4 above it, so a weight is at most 1 (a larger one could
+// overflow beside values near fp32's largest) and most steps rescale nothing.
 #pragma once
 
 #include <algorithm>
@@ -59,10 +60,10 @@ constexpr int kLaneUnits = 8;          // units of a lane where a warp scans the
 // alone: 16 heads x 32,000 rows 48 us in clusters of four, 51 on the line.
 constexpr long long kClusterSlack = 4;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
-// The level that a column's weights are relative to follows its running maximum only when that
-// has grown by more than this (base 2): most steps then rescale nothing.
+// The level that a column's weights are relative to is set this far (base 2) above the running
+// maximum when that passes it: most steps then rescale nothing.
 constexpr float kSlack = 4.f;
-constexpr float kShift16 = 10.f;       // f16 weights are at most 2^(10 + kSlack) (fp16 ends at 2^16)
+constexpr float kShift16 = 15.f;       // f16 weights are at most 2^15 (fp16 ends at 2^16)
 
 // A segment: its sequence, kv head and first query row, its steps, and where it starts on the
 // line (which tells segments apart).
@@ -122,6 +123,8 @@ SA_DEVI float col_sum(float x) {
   x += __shfl_xor_sync(~0u, x, 8);
   return x + __shfl_xor_sync(~0u, x, 16);
 }
+// A column's level, given a step's maximum.
+SA_DEVI float level(float x, float m) { return x > m ? x + kSlack : m; }
 // A maximum to subtract: 0 while nothing was attended (-inf - -inf would be NaN).
 SA_DEVI float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -487,7 +490,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
       }
     }
     // running maxima: the warp looks across its lanes, and rescales, only when one of its
-    // columns has outgrown its level
+    // columns has passed its level
     float nm[NT][2], nv[NT][2];
     bool moved = false;
 #pragma unroll
@@ -503,19 +506,19 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         }
         nm[nt][i] = x;
         nv[nt][i] = y;
-        moved |= x > m[nt][i] + kSlack;
-        if constexpr (E4M3) moved |= y > mv[nt][i] + kSlack;
+        moved |= x > m[nt][i];
+        if constexpr (E4M3) moved |= y > mv[nt][i];
       }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          nm[nt][i] = col_max(fmaxf(nm[nt][i], m[nt][i]));
+          nm[nt][i] = level(col_max(nm[nt][i]), m[nt][i]);
           const float a = ex2a(m[nt][i] - ref_of(nm[nt][i]));
           float c = a;
           if constexpr (E4M3) {
-            nv[nt][i] = col_max(fmaxf(nv[nt][i], mv[nt][i]));
+            nv[nt][i] = level(col_max(nv[nt][i]), mv[nt][i]);
             c = ex2a(mv[nt][i] - ref_of(nv[nt][i]));
             mv[nt][i] = nv[nt][i];
           }

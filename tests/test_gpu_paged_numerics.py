@@ -45,3 +45,24 @@ def test_values_near_the_smallest(n, page, out_dtype):
         out, lse = P.decode(q, c, _ints(table), _ints([n]), out_dtype=out_dtype, return_lse=True)
         _check(out, lse, out_dtype, d, 1 / np.sqrt(d), q, c, table, [n], page)
         assert out.any(-1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,Hq", [(200, 1), (9001, 12), (300, 20)])
+def test_values_near_the_largest(n, Hq, dtype):
+    """V of 3e38 at keys that outweigh what came before them by up to 2^4: the product of a
+    weight and a value must not overflow where their share of the output does not."""
+    rng = np.random.default_rng(3)
+    d, page = 128, 32
+    k = torch.zeros(1, 1, n, d, dtype=BF16, device="cuda")
+    v = _bf16(rng, 1, 1, n, d)
+    q = torch.zeros(1, Hq, 1, d, dtype=BF16, device="cuda")
+    q[..., 0] = 1
+    for i, bits in ((n // 2, 1.0), (n - 20, 3.5)):
+        k[0, 0, i, 0] = bits * np.log(2)
+        v[0, 0, i] = 0
+        v[0, 0, i, ::5] = 3.0e38 * (1 if i % 2 else -1)
+    c, table = _cache(k, v, page, dtype)
+    out, lse = P.decode(q, c, _ints(table), _ints([n]), scale=1.0, return_lse=True)
+    assert out.isfinite().all()
+    _check(out, lse, F32, d, 1.0, q, c, table, [n], page)
