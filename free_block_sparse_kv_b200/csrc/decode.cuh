@@ -33,7 +33,7 @@
 // (5.4-5.2 TB/s).
 //
 // Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
-// before: as many as keep the dropped rest below the output's own rounding (run_decode()).
+// before: as many as keep the dropped rest below the output's own rounding (Math::PIECES).
 // e4m3 codes enter as f16, exactly; the query then enters as f16 times a power of two per row
 // that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that value). The
 // scale of a V row is folded into its weight: numerator weights carry their own level, the
@@ -216,10 +216,21 @@ SA_DEVI void scales(const Step& w, int lane) {
 // The arithmetic of a warp: 16-bit products of bf16 rows as they are, or of e4m3 codes as f16
 // (mma.sync has no 8-bit form on this architecture that is not these conversions done again
 // for every product). A lane owns the columns (query rows) 2q and 2q + 1 of each n-tile of
-// eight, and two keys of each 16-key tile. PIECES: 16-bit pieces that a weight takes.
-template <int D, bool E4M3, int PIECES, int NT, int WARPS, int STAGES>
+// eight, and two keys of each 16-key tile. F32: the output is fp32.
+template <int D, bool E4M3, bool F32, int NT, int WARPS, int STAGES>
 struct Math : Layout<D, E4M3, WARPS, STAGES> {
   using L = Layout<D, E4M3, WARPS, STAGES>;
+  // 16-bit pieces of a weight: as many as keep what they drop below the output's own rounding
+  // (half a step: 2^-8 of a bf16 value at most, 2^-24 of fp32): one f16 piece drops 2^-11 of a
+  // weight at most and two bf16 pieces 2^-16; for fp32 outputs two f16 pieces drop 2^-22 and
+  // three bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds.
+  static constexpr int PIECES = (E4M3 ? 1 : 2) + F32;
+  // The tensor cores cut the bits of a sum off where fp32 ends, which pulls a long chain
+  // towards zero: 6e-5 of a sum of one sign after 1,900 steps, far below what a bf16 output
+  // rounds. For fp32 outputs the products of a step (with 16 rows and more, a tile) are summed
+  // there, and the steps added to nearest here: 4 x 16 heads x 63,960 bf16 rows 302 us against
+  // 300, 40 heads x 75,600 e4m3 rows 131 against 125, 32 bf16 rows a segment 48.2 against 46.0.
+  static constexpr bool kAdds = F32;
   static constexpr int kRows = 8 * NT, kMt = D / 16;
   // With 32 rows the queries would take 64 registers of a lane: they stay in shared memory.
   static constexpr bool kQs = NT == 4;
@@ -236,7 +247,14 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   uint32_t qs;                     // this warp's queries in shared memory (kQs, kAhead)
   int r0, len, R;
   float m[NT][2], l[NT][2], mv[NT][2], f[NT][2];
-  int lim[NT][2];
+  float unit;                      // scale in base 2
+  // How many positions a column's row attends; with 32 rows four bits a column hold how many
+  // it does not (registers: 184 bytes spilled against 24).
+  int lims[kQs ? 1 : NT][2];
+  uint32_t before;
+  SA_DEVI int lim(int nt, int i) const {
+    return kQs ? len - (int)(before >> (8 * nt + 4 * i) & 15u) : lims[kQs ? 0 : nt][i];
+  }
   float o[kMt][NT][4];
   int lane, q4, r8;
 
@@ -346,6 +364,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   }
   SA_DEVI void start(const DecodeArgs& p) {
     if constexpr (kQs && E4M3) convert_queries(p);
+    before = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float back = 1.f;     // of row r8
@@ -358,9 +377,12 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
                        : "=f"(f[nt][i]) : "r"(qs + kRows * D * 2 + (nt * 8 + 2 * q4 + i) * 4) : "memory");
         else if constexpr (E4M3)
           f[nt][i] = __shfl_sync(~0u, back, (2 * q4 + i) * 4);
-        f[nt][i] *= p.scale * kLog2e;
+        unit = p.scale * kLog2e;
+        f[nt][i] *= unit;
         const int rc = r0 + nt * 8 + 2 * q4 + i;
-        lim[nt][i] = len - (rc < R ? p.T - 1 - rc % p.T : 0);
+        const int unseen = rc < R ? p.T - 1 - rc % p.T : 0;
+        before |= (uint32_t)unseen << (8 * nt + 4 * i);
+        if constexpr (!kQs) lims[nt][i] = len - unseen;
       }
     }
 #pragma unroll
@@ -377,6 +399,20 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     }
   }
 
+  SA_DEVI static void mma_first(float* d, const uint32_t* a, const uint32_t* b) {   // on zeros
+    if constexpr (E4M3)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+          "{%10,%10,%10,%10};\n"
+          : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+          "{%10,%10,%10,%10};\n"
+          : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+  }
   SA_DEVI static void mma(float* d, const uint32_t* a, const uint32_t* b) {
     if constexpr (E4M3) mma_f16(d, a, b[0], b[1]); else mma_bf16(d, a, b[0], b[1]);
   }
@@ -472,7 +508,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = s[t][nt][i] * f[nt][i & 1];
+          float x = s[t][nt][i] * (kQs && !E4M3 ? unit : f[nt][i & 1]);
           if constexpr (E4M3) x *= ks[i >> 1];
           s[t][nt][i] = x;
           if constexpr (E4M3) sv[t][nt][i] = x + vl[i >> 1];
@@ -483,7 +519,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (pos0 + L::kKeyStep * (i >> 1) >= lim[nt][i & 1]) {
+            if (pos0 + L::kKeyStep * (i >> 1) >= lim(nt, i & 1)) {
               s[t][nt][i] = -INFINITY;
               if constexpr (E4M3) sv[t][nt][i] = -INFINITY;
             }
@@ -534,10 +570,10 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     // V's addresses: bf16 as 8x8 blocks (keys mi>>1, values mi&1), e4m3 as two 16x16 blocks
     const uint32_t va = E4M3 ? w.v + swz_row<L::kRow>(L::place(lane & 15), lane >> 4)
                              : w.v + swz_row<L::kRow>(mr + (mi >> 1) * 8, mi & 1);
+    // B = P^T in pieces, by transposing each 8x8 block of S^T
+    uint32_t pw[SUB][PIECES][NT][2];
 #pragma unroll
-    for (int t = 0; t < SUB; ++t) {
-      // B = P^T in pieces, by transposing each 8x8 block of S^T
-      uint32_t pw[PIECES][NT][2];
+    for (int t = 0; t < SUB; ++t)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -563,45 +599,71 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
               e[0] -= bf16_lo(hi);
               e[1] -= bf16_hi(hi);
             }
-            pw[k][nt][hf] = movmatrix(hi);
+            pw[t][k][nt][hf] = movmatrix(hi);
           }
         }
-      // A = V^T, 32 output columns at a time
-      auto load_v = [&](int x, uint32_t (&a)[2][4]) {
-        if constexpr (E4M3) {
-          uint32_t y[4];
-          ldsm_t8((va ^ (uint32_t)(2 * x << 4)) + (t0 + t) * 16 * L::kRow, y);
+    // A = V^T, 32 output columns at a time
+    auto load_v = [&](int t, int x, uint32_t (&a)[2][4]) {
+      if constexpr (E4M3) {
+        uint32_t y[4];
+        ldsm_t8((va ^ (uint32_t)(2 * x << 4)) + (t0 + t) * 16 * L::kRow, y);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              a[i][j] = e4m3x2_to_f16x2(y[2 * i + j]);
-              a[i][2 + j] = e4m3x2_to_f16x2(y[2 * i + j] >> 16);
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            ldsm_x4_t((va ^ (uint32_t)(2 * (2 * x + i) << 4)) + (t0 + t) * 16 * L::kRow, a[i][0], a[i][1],
-                      a[i][2], a[i][3]);
-        }
-      };
-      if (w.all || !w.part(t0 + t) || finite_values(w, t0 + t)) {
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t a[2][4];
-          load_v(x, a);
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int k = 0; k < PIECES; ++k) mma(o[x * 2 + y][nt], a[y], pw[k][nt]);
-            }
-        }
+          for (int j = 0; j < 2; ++j) {
+            a[i][j] = e4m3x2_to_f16x2(y[2 * i + j]);
+            a[i][2 + j] = e4m3x2_to_f16x2(y[2 * i + j] >> 16);
+          }
       } else {
-        // New tokens that some rows attend and others do not, with a non-finite value: a
-        // zero weight times it would reach the others, so each token's rows take a product
-        // of their own in which the values that they do not attend are zeros.
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ldsm_x4_t((va ^ (uint32_t)(2 * (2 * x + i) << 4)) + (t0 + t) * 16 * L::kRow, a[i][0], a[i][1],
+                    a[i][2], a[i][3]);
+      }
+    };
+    bool clean = true;   // no tile that some rows attend and others do not has a non-finite value
+    if (!w.all)
+#pragma unroll 1
+      for (int t = 0; t < SUB && clean; ++t) clean = !w.part(t0 + t) || finite_values(w, t0 + t);
+    if (clean) {
+      // (two columns' chains side by side for one n-tile, all n-tiles' for more)
+      constexpr int Y = NT == 1 ? 2 : 1;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t a[SUB][2][4];
+#pragma unroll
+        for (int t = 0; t < SUB; ++t) load_v(t, x, a[t]);
+#pragma unroll
+        for (int y0 = 0; y0 < 2; y0 += Y) {
+          float z[Y][NT][4];
+#pragma unroll
+          for (int t = 0; t < SUB; ++t)
+#pragma unroll
+            for (int k = 0; k < PIECES; ++k)
+#pragma unroll
+              for (int y = 0; y < Y; ++y)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (!kAdds) mma(o[x * 2 + y0 + y][nt], a[t][y0 + y], pw[t][k][nt]);
+                  else if (t == 0 && k == 0) mma_first(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
+                  else mma(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
+                }
+          if constexpr (kAdds) {
+#pragma unroll
+            for (int y = 0; y < Y; ++y)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[x * 2 + y0 + y][nt][i] += z[y][nt][i];
+          }
+        }
+      }
+    } else {
+      // New tokens that some rows attend and others do not, with a non-finite value: a
+      // zero weight times it would reach the others, so each token's rows take a product
+      // of their own in which the values that they do not attend are zeros.
+#pragma unroll
+      for (int t = 0; t < SUB; ++t)
 #pragma unroll 1
         for (int tok = 0; tok < w.T; ++tok) {
           const int mine = w.len - (w.T - 1 - tok);
@@ -614,7 +676,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
             uint32_t a[2][4];
-            load_v(x, a);
+            load_v(t, x, a);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
 #pragma unroll
@@ -623,15 +685,14 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
               for (int nt = 0; nt < NT; ++nt) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < PIECES; ++k) mma(z, a[y], pw[k][nt]);
+                for (int k = 0; k < PIECES; ++k) mma(z, a[y], pw[t][k][nt]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (lim[nt][i & 1] == mine) o[x * 2 + y][nt][i] += z[i];
+                  if (lim(nt, i & 1) == mine) o[x * 2 + y][nt][i] += z[i];
               }
             }
           }
         }
-      }
     }
   }
 
@@ -1449,26 +1510,22 @@ cudaError_t run(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_wo
 
 // The fewest rows per segment that hold the R rows of a kv head, up to 32 (more take further
 // segments, which read the keys again).
-template <int D, bool E4M3, int PIECES>
+template <int D, bool E4M3, bool F32>
 cudaError_t run_rows(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_work) {
   const long long R = (long long)(p.Hq / p.c.H) * p.T;
-  if (R <= 8) return run<D, Math<D, E4M3, PIECES, 1, 12, 2>>(p, st, bytes, no_work);
-  if (R <= 16) return run<D, Math<D, E4M3, PIECES, 2, 8, 3>>(p, st, bytes, no_work);
-  return run<D, Math<D, E4M3, PIECES, 4, 8, 2>>(p, st, bytes, no_work);
+  if (R <= 8) return run<D, Math<D, E4M3, F32, 1, 12, 2>>(p, st, bytes, no_work);
+  if (R <= 16) return run<D, Math<D, E4M3, F32, 2, 8, 3>>(p, st, bytes, no_work);
+  return run<D, Math<D, E4M3, F32, 4, 8, 2>>(p, st, bytes, no_work);
 }
 
 }  // namespace
 
-// Pieces of a weight: as many as keep what they drop below the output's own rounding (half a
-// step: 2^-8 of a bf16 value at most, 2^-24 of fp32): one f16 piece drops 2^-11 of a weight
-// at most and two bf16 pieces 2^-16; for fp32 outputs two f16 pieces drop 2^-22 and three
-// bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds.
 template <int D>
 cudaError_t run_decode(const DecodeArgs& p, cudaStream_t st, size_t* bytes, bool* no_work) {
   const bool f32 = p.out_dtype == SA_OUT_F32;
   if (p.c.e4m3)
-    return f32 ? run_rows<D, true, 2>(p, st, bytes, no_work) : run_rows<D, true, 1>(p, st, bytes, no_work);
-  return f32 ? run_rows<D, false, 3>(p, st, bytes, no_work) : run_rows<D, false, 2>(p, st, bytes, no_work);
+    return f32 ? run_rows<D, true, true>(p, st, bytes, no_work) : run_rows<D, true, false>(p, st, bytes, no_work);
+  return f32 ? run_rows<D, false, true>(p, st, bytes, no_work) : run_rows<D, false, false>(p, st, bytes, no_work);
 }
 
 }  // namespace sa

@@ -66,3 +66,34 @@ def test_values_near_the_largest(n, Hq, dtype):
     out, lse = P.decode(q, c, _ints(table), _ints([n]), scale=1.0, return_lse=True)
     assert out.isfinite().all()
     _check(out, lse, F32, d, 1.0, q, c, table, [n], page)
+
+
+@pytest.mark.parametrize("B,G,T,H,pages", [(8, 1, 1, 4, 3200), (8, 16, 1, 4, 3200), (4, 8, 4, 2, 9000)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_long_sums(B, G, T, H, pages, dtype):
+    """Hundreds of steps a warp over columns of V that each hold one value: the output is that
+    value. A step's products are a short chain on the tensor cores (their sums lose at most
+    2^-23 each, all to one side: 4 in a row at most), and the steps are added to nearest: S of
+    them into a sum that grows evenly are off by u sqrt(S / 9) in the mean square, the sum of
+    weights as much; six times that. The pieces of a weight keep 2^-22 of it."""
+    rng = np.random.default_rng(G + T)
+    d, page, num = 128, 256, 24
+    n = pages * page
+    c = P.allocate_cache(num, H, page, d, dtype)
+    k = _bf16(rng, 1, H, num * page, d)
+    col = _bf16(rng, 1, H, 1, d).abs() + 0.5        # of one exponent's size: 8 bits keep 4 of them
+    col = col.to(E4M3).to(BF16)
+    rows = list(range(num))
+    P.cache_append(c, k, col.expand(1, H, num * page, d), _ints([rows]), _ints([0]))
+    table = _ints(rng.integers(0, num, (B, pages)))  # pages that are only read may be shared
+    q = _bf16(rng, B, G * H, T, d)
+    out, lse = P.decode(q, c, table, _ints([n] * B), return_lse=True)
+    want = torch.empty(1, H, num * page, d, dtype=BF16, device="cuda")
+    P.cache_read(c, _ints([rows]), _ints([num * page]), torch.empty_like(want), want)
+    want = want[:, :, :1].double().repeat_interleave(G, 1)
+    # steps of a warp: the line has at least 8 warps on each of at least 132 SMs
+    steps = B * H * -(-G * T // 32) * n * d * (1 if dtype == E4M3 else 2) / 4096 / (132 * 8)
+    tol = 2.0 ** -22 + 4 * 2.0 ** -23 + 6 * 2.0 ** -24 * np.sqrt(2 * steps / 9)
+    assert steps > 500
+    err = ((out.double() - want) / want).abs().max().item()
+    assert err <= tol, (err, tol)
