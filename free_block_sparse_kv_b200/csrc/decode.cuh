@@ -35,11 +35,15 @@
 // Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
 // before: as many as keep the dropped rest below the output's own rounding (Math::PIECES).
 // e4m3 codes enter as f16, exactly; the query then enters as f16 times a power of two per row
-// that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that value). The
-// scale of a V row is folded into its weight: numerator weights carry their own level, the
-// running maximum of l_p + log2(scale_p), so that no scale can overflow or starve them. A level
+// that brings its largest value to 2^14 (what f16 drops is below 2^-38 of that value). A level
 // that a running maximum passes is set 2^4 above it, so a weight is at most 1 (a larger one could
 // overflow beside values near fp32's largest) and most steps rescale nothing.
+// The scale of a V row, a power of two, multiplies its weight: exactly, relative to the largest
+// scale so far, so that the largest weight lies between 2^11 and 2^15 of f16's range. f16 rounds
+// to 2^-25 at least, which is 2^-36 of the largest weight for rows of that scale. Rows whose
+// scale is far below it (a V row with an outlier raises it for every column) would fall out of
+// that range: a step that holds one converts its codes and weights to bf16 pieces instead, whose
+// range is fp32's (Math::kFar).
 #pragma once
 
 #include <algorithm>
@@ -63,7 +67,8 @@ constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 // The level that a column's weights are relative to is set this far (base 2) above the running
 // maximum when that passes it: most steps then rescale nothing.
 constexpr float kSlack = 4.f;
-constexpr float kShift16 = 15.f;       // f16 weights are at most 2^15 (fp16 ends at 2^16)
+constexpr int kShift16 = 15;           // f16 weights are at most 2^15 (fp16 ends at 2^16)
+constexpr int kNoLevel = -1000;        // no V row seen
 
 // A segment: its sequence, kv head and first query row, its steps, and where it starts on the
 // line (which tells segments apart).
@@ -108,6 +113,10 @@ SA_DEVI uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
   return d;
 }
+SA_DEVI uint32_t f16x2_to_bf16x2(uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pack_bf16(f.x, f.y);
+}
 SA_DEVI float ex2a(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -145,7 +154,7 @@ struct Step {
   uint32_t k, v;
   const uint8_t* vp;      // V rows, generic
   const uint8_t* meta;
-  float2* sc;             // e4m3: (K scale, log2 of V scale) of every key, made by scales()
+  float2* sc;             // e4m3: (K scale, factor of the weight) of every key, made by scales()
   int len, T;
   bool all;               // every key of the step is attended by every row
   SA_DEVI int pos(int t) const { return reinterpret_cast<const int*>(meta + 128)[t]; }
@@ -188,30 +197,8 @@ struct Layout {
   }
 };
 
-// The scales of a step's keys as values, a key to a lane. A row of zeros is stored with scale
-// 1; it adds nothing to the numerator, and must not set the level that the other rows'
-// weights are held at: its log2 scale becomes -inf.
-template <class L>
-SA_DEVI void scales(const Step& w, int lane) {
-#pragma unroll
-  for (int key = lane; key < L::kKeys; key += 32) {
-    const uint32_t kb = w.meta[key], vb = w.meta[L::kKeys + key];
-    float lv = __uint_as_float(0x4B000000u | vb) - 8388735.f;    // vb - 127
-    if (vb == 255u) lv = __uint_as_float(0x7FC00000u);
-    if (vb == 127u) {
-      const int row = (key & ~15) + L::place(key & 15);
-      uint32_t any = 0;
-#pragma unroll 1
-      for (int c = 0; c < L::kChunks; ++c) {
-        const uint4 y = *reinterpret_cast<const uint4*>(w.vp + swz_row<L::kRow>(row, c));
-        any |= (y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu;
-      }
-      if (any == 0) lv = -INFINITY;
-    }
-    w.sc[key] = make_float2(e8m0_value(kb), lv);
-  }
-  __syncwarp();
-}
+// 2^e; 0 below fp32's smallest normal value.
+SA_DEVI float pow2(int e) { return __uint_as_float(e < -126 ? 0u : (uint32_t)(e + 127) << 23); }
 
 // The arithmetic of a warp: 16-bit products of bf16 rows as they are, or of e4m3 codes as f16
 // (mma.sync has no 8-bit form on this architecture that is not these conversions done again
@@ -223,7 +210,9 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   // 16-bit pieces of a weight: as many as keep what they drop below the output's own rounding
   // (half a step: 2^-8 of a bf16 value at most, 2^-24 of fp32): one f16 piece drops 2^-11 of a
   // weight at most and two bf16 pieces 2^-16; for fp32 outputs two f16 pieces drop 2^-22 and
-  // three bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds.
+  // three bf16 pieces 2^-24. One bf16 piece would drop as much as the bf16 output rounds. One
+  // f16 piece leaves bf16 outputs 0.1610% from 64 bits in the mean where the rounding alone
+  // leaves 0.1604%; a second would take 4 to 16% more time (4 to 32 rows).
   static constexpr int PIECES = (E4M3 ? 1 : 2) + F32;
   // The tensor cores cut the bits of a sum off where fp32 ends, which pulls a long chain
   // towards zero: 6e-5 of a sum of one sign after 1,900 steps, far below what a bf16 output
@@ -246,7 +235,15 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   uint32_t qf[kQs ? 1 : NT][D / 16][2];
   uint32_t qs;                     // this warp's queries in shared memory (kQs, kAhead)
   int r0, len, R;
-  float m[NT][2], l[NT][2], mv[NT][2], f[NT][2];
+  float m[NT][2], l[NT][2], f[NT][2];
+  // e4m3: o is in units of 2^(top - kShift16). The largest scale of the V rows so far, as log2.
+  int top;
+  // Rows whose scale is more than 2^kFar below it take their step to bf16 pieces. Within it a
+  // weight is rounded to 2^(kFar - 36) of the largest one or better; were 65,536 rows to err to
+  // one side, that were 2^-16 of the sum for fp32 outputs and 2^-12 for bf16 ones. The scales of
+  // rows of normally distributed values differ by 2^1. 40 heads x 75,600 rows, one row in 1,000
+  // scaled up by 2^8: fp32 outputs 169 us against 130, bf16 outputs 146 against 127.
+  static constexpr int kFar = F32 ? 4 : 8;
   float unit;                      // scale in base 2
   // How many positions a column's row attends; with 32 rows four bits a column hold how many
   // it does not (registers: 184 bytes spilled against 24).
@@ -365,6 +362,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   SA_DEVI void start(const DecodeArgs& p) {
     if constexpr (kQs && E4M3) convert_queries(p);
     before = 0;
+    top = kNoLevel;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float back = 1.f;     // of row r8
@@ -389,7 +387,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        m[nt][i] = mv[nt][i] = -INFINITY;
+        m[nt][i] = -INFINITY;
         l[nt][i] = 0.f;
       }
 #pragma unroll
@@ -399,8 +397,9 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     }
   }
 
+  template <bool F16>
   SA_DEVI static void mma_first(float* d, const uint32_t* a, const uint32_t* b) {   // on zeros
-    if constexpr (E4M3)
+    if constexpr (F16)
       asm volatile(
           "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
           "{%10,%10,%10,%10};\n"
@@ -413,8 +412,9 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
           : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
           : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
   }
+  template <bool F16>
   SA_DEVI static void mma(float* d, const uint32_t* a, const uint32_t* b) {
-    if constexpr (E4M3) mma_f16(d, a, b[0], b[1]); else mma_bf16(d, a, b[0], b[1]);
+    if constexpr (F16) mma_f16(d, a, b[0], b[1]); else mma_bf16(d, a, b[0], b[1]);
   }
   // The operands of 32 columns of n-tile nt: two per 16.
   SA_DEVI void queries(int nt, int pair, uint32_t (&b)[2][2]) {
@@ -444,18 +444,87 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
     return !__any_sync(~0u, bad & (E4M3 ? 0x80808080u : 0x80008000u));
   }
 
+  // The scales of a step's keys, a key to a lane: the K scale, and the V scale relative to the
+  // largest so far. A row of zeros (append stores scale 1) adds nothing and is no reason for
+  // another level; rows behind the last one hold anything. New tokens that some rows do not
+  // attend leave the level alone as far as fp32's range allows, so that those rows keep their
+  // bits: they belong to the last step of a sequence, which is held in bf16 pieces. Returns
+  // whether the step is.
+  SA_DEVI bool scales(const Step& w) {
+    constexpr int PER = L::kKeys / 32;
+    uint32_t kb[PER];
+    int lv[PER], pos[PER];
+    bool dead[PER], odd = !w.all && w.T > 1, wide = false;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int key = j * 32 + lane;
+      kb[j] = w.meta[key];
+      lv[j] = (int)w.meta[L::kKeys + key] - 127;
+      pos[j] = w.all ? 0 : w.pos(key >> 4) + (key & 15);
+      dead[j] = !w.all && pos[j] >= w.len;
+      if (lv[j] == 0) {
+        const int row = (key & ~15) + L::place(key & 15);
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int c = 0; c < L::kChunks; ++c) {
+          const uint4 y = *reinterpret_cast<const uint4*>(w.vp + swz_row<L::kRow>(row, c));
+          any |= (y.x | y.y | y.z | y.w) & 0x7F7F7F7Fu;
+        }
+        dead[j] |= any == 0;
+      }
+      odd |= !dead[j] && lv[j] != 128 && (uint32_t)(top - lv[j]) > (uint32_t)kFar;
+    }
+    if (__any_sync(~0u, odd)) {     // a scale above the level or far below it, or new tokens
+      int most = kNoLevel, late = kNoLevel, least = -kNoLevel;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if (dead[j] || lv[j] == 128) continue;
+        if (w.all || pos[j] < w.len - w.T + 1) most = max(most, lv[j]);
+        else late = max(late, lv[j]);
+        least = min(least, lv[j]);
+      }
+      most = __reduce_max_sync(~0u, most);
+      late = __reduce_max_sync(~0u, late);
+      least = __reduce_min_sync(~0u, least);
+      most = max(most, late - 96);
+      if (most > top) {
+        if (top != kNoLevel) {
+          const int d = top - most, h = d >> 1;
+          const float a = pow2(h), b = pow2(d - h);
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[mt][nt][i] = o[mt][nt][i] * a * b;
+        }
+        top = most;
+      }
+      wide = (!w.all && w.T > 1) || least < top - kFar;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const float g = dead[j] ? 0.f : lv[j] == 128 ? __uint_as_float(0x7FC00000u)
+                                                   : pow2(lv[j] - top + kShift16);
+      w.sc[j * 32 + lane] = make_float2(e8m0_value(kb[j]), g);
+    }
+    __syncwarp();
+    return wide;
+  }
+
   SA_DEVI void compute(const Step& w) {
-    if constexpr (E4M3) scales<L>(w, lane);
+    bool wide = false;
+    if constexpr (E4M3) wide = scales(w);
     // one n-tile: all tiles of the step together; more: one after the other, for the registers
     constexpr int AT_ONCE = NT == 1 ? L::kSub : 1;
 #pragma unroll 1
-    for (int t0 = 0; t0 < L::kSub; t0 += AT_ONCE) tiles<AT_ONCE>(w, t0);
+    for (int t0 = 0; t0 < L::kSub; t0 += AT_ONCE) tiles<AT_ONCE>(w, t0, wide);
   }
 
   template <int SUB>
-  SA_DEVI void tiles(const Step& w, int t0) {
+  SA_DEVI void tiles(const Step& w, int t0, bool wide) {
     float s[SUB][NT][4];
-    float sv[E4M3 ? SUB : 1][NT][4];   // s + log2 of the key's V scale
+    float g[E4M3 ? SUB : 1][2];        // factor of the weights of the lane's keys
     const int mi = lane >> 3, mr = lane & 7, key = L::key_of(r8);
     const uint32_t ka = w.k + swz_row<L::kRow>(mr + (mi & 1) * 8, mi >> 1);
 #pragma unroll
@@ -490,18 +559,18 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t b[2][2];
           queries(nt, x, b);
-          mma(s[t][nt], a[0], b[0]);
-          mma(s[t][nt], a[1], b[1]);
+          mma<E4M3>(s[t][nt], a[0], b[0]);
+          mma<E4M3>(s[t][nt], a[1], b[1]);
         }
       }
       // scale to base 2 and mask
-      float ks[2] = {1.f, 1.f}, vl[2] = {0.f, 0.f};
+      float ks[2] = {1.f, 1.f};
       if constexpr (E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float2 sc = w.sc[(t0 + t) * 16 + key + L::kKeyStep * i];
           ks[i] = sc.x;
-          vl[i] = sc.y;
+          g[t][i] = sc.y;
         }
       }
 #pragma unroll
@@ -511,7 +580,6 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
           float x = s[t][nt][i] * (kQs && !E4M3 ? unit : f[nt][i & 1]);
           if constexpr (E4M3) x *= ks[i >> 1];
           s[t][nt][i] = x;
-          if constexpr (E4M3) sv[t][nt][i] = x + vl[i >> 1];
         }
       if (!w.all) {
         const int pos0 = w.pos(t0 + t) + key;
@@ -519,31 +587,22 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (pos0 + L::kKeyStep * (i >> 1) >= lim(nt, i & 1)) {
-              s[t][nt][i] = -INFINITY;
-              if constexpr (E4M3) sv[t][nt][i] = -INFINITY;
-            }
+            if (pos0 + L::kKeyStep * (i >> 1) >= lim(nt, i & 1)) s[t][nt][i] = -INFINITY;
       }
     }
     // running maxima: the warp looks across its lanes, and rescales, only when one of its
     // columns has passed its level
-    float nm[NT][2], nv[NT][2];
+    float nm[NT][2];
     bool moved = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(s[0][nt][i], s[0][nt][i + 2]), y = 0.f;
-        if constexpr (E4M3) y = fmaxf(sv[0][nt][i], sv[0][nt][i + 2]);
+        float x = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
 #pragma unroll
-        for (int t = 1; t < SUB; ++t) {
-          x = fmaxf(x, fmaxf(s[t][nt][i], s[t][nt][i + 2]));
-          if constexpr (E4M3) y = fmaxf(y, fmaxf(sv[t][nt][i], sv[t][nt][i + 2]));
-        }
+        for (int t = 1; t < SUB; ++t) x = fmaxf(x, fmaxf(s[t][nt][i], s[t][nt][i + 2]));
         nm[nt][i] = x;
-        nv[nt][i] = y;
         moved |= x > m[nt][i];
-        if constexpr (E4M3) moved |= y > mv[nt][i];
       }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -552,44 +611,57 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
         for (int i = 0; i < 2; ++i) {
           nm[nt][i] = level(col_max(nm[nt][i]), m[nt][i]);
           const float a = ex2a(m[nt][i] - ref_of(nm[nt][i]));
-          float c = a;
-          if constexpr (E4M3) {
-            nv[nt][i] = level(col_max(nv[nt][i]), mv[nt][i]);
-            c = ex2a(mv[nt][i] - ref_of(nv[nt][i]));
-            mv[nt][i] = nv[nt][i];
-          }
           l[nt][i] *= a;
           m[nt][i] = nm[nt][i];
 #pragma unroll
           for (int mt = 0; mt < kMt; ++mt) {
-            o[mt][nt][i] *= c;
-            o[mt][nt][i + 2] *= c;
+            o[mt][nt][i] *= a;
+            o[mt][nt][i + 2] *= a;
           }
         }
     }
+    // weights, and what of them goes to the sum
+#pragma unroll
+    for (int t = 0; t < SUB; ++t)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = s[t][nt][i], e = ex2a(x - ref_of(m[nt][i & 1]));
+          l[nt][i & 1] += e;
+          // (a factor of NaN must not reach the rows that do not attend its key)
+          s[t][nt][i] = !E4M3 ? e : w.all || x != -INFINITY ? e * g[E4M3 ? t : 0][i >> 1] : 0.f;
+        }
+    if (E4M3 && wide) {
+#pragma unroll
+      for (int t = 0; t < SUB; ++t) products<1, true>(w, t0 + t, s + t);
+    } else {
+      products<SUB, false>(w, t0, s);
+    }
+  }
+
+  // o += P V over SUB tiles from t0 on. WIDE (e4m3): both in bf16, the weights in three pieces.
+  template <int SUB, bool WIDE>
+  SA_DEVI void products(const Step& w, int t0, float (*s)[NT][4]) {
+    constexpr bool F16 = E4M3 && !WIDE;
+    constexpr int PC = WIDE ? 3 : PIECES;
+    const int mi = lane >> 3, mr = lane & 7;
     // V's addresses: bf16 as 8x8 blocks (keys mi>>1, values mi&1), e4m3 as two 16x16 blocks
     const uint32_t va = E4M3 ? w.v + swz_row<L::kRow>(L::place(lane & 15), lane >> 4)
                              : w.v + swz_row<L::kRow>(mr + (mi >> 1) * 8, mi & 1);
     // B = P^T in pieces, by transposing each 8x8 block of S^T
-    uint32_t pw[SUB][PIECES][NT][2];
+    uint32_t pw[SUB][PC][NT][2];
 #pragma unroll
     for (int t = 0; t < SUB; ++t)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float e[2];
+          float e[2] = {s[t][nt][2 * hf], s[t][nt][2 * hf + 1]};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            e[i] = ex2a(s[t][nt][2 * hf + i] - ref_of(m[nt][i]));
-            l[nt][i] += e[i];
-            if constexpr (E4M3)
-              e[i] = ex2a(sv[t][nt][2 * hf + i] - (ref_of(mv[nt][i]) - kShift16));
-          }
-#pragma unroll
-          for (int k = 0; k < PIECES; ++k) {
+          for (int k = 0; k < PC; ++k) {
             uint32_t hi;
-            if constexpr (E4M3) {
+            if constexpr (F16) {
               hi = pack_f16(e[0], e[1]);
               const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
               e[0] -= b.x;
@@ -613,6 +685,10 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
           for (int j = 0; j < 2; ++j) {
             a[i][j] = e4m3x2_to_f16x2(y[2 * i + j]);
             a[i][2 + j] = e4m3x2_to_f16x2(y[2 * i + j] >> 16);
+            if constexpr (WIDE) {
+              a[i][j] = f16x2_to_bf16x2(a[i][j]);
+              a[i][2 + j] = f16x2_to_bf16x2(a[i][2 + j]);
+            }
           }
       } else {
 #pragma unroll
@@ -622,7 +698,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
       }
     };
     bool clean = true;   // no tile that some rows attend and others do not has a non-finite value
-    if (!w.all)
+    if (!F16 && !w.all)     // (e4m3: such tiles come here WIDE)
 #pragma unroll 1
       for (int t = 0; t < SUB && clean; ++t) clean = !w.part(t0 + t) || finite_values(w, t0 + t);
     if (clean) {
@@ -639,14 +715,14 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
 #pragma unroll
           for (int t = 0; t < SUB; ++t)
 #pragma unroll
-            for (int k = 0; k < PIECES; ++k)
+            for (int k = 0; k < PC; ++k)
 #pragma unroll
               for (int y = 0; y < Y; ++y)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (!kAdds) mma(o[x * 2 + y0 + y][nt], a[t][y0 + y], pw[t][k][nt]);
-                  else if (t == 0 && k == 0) mma_first(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
-                  else mma(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
+                  if (!kAdds) mma<F16>(o[x * 2 + y0 + y][nt], a[t][y0 + y], pw[t][k][nt]);
+                  else if (t == 0 && k == 0) mma_first<F16>(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
+                  else mma<F16>(z[y][nt], a[t][y0 + y], pw[t][k][nt]);
                 }
           if constexpr (kAdds) {
 #pragma unroll
@@ -658,7 +734,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
           }
         }
       }
-    } else {
+    } else if constexpr (!F16) {
       // New tokens that some rows attend and others do not, with a non-finite value: a
       // zero weight times it would reach the others, so each token's rows take a product
       // of their own in which the values that they do not attend are zeros.
@@ -685,7 +761,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
               for (int nt = 0; nt < NT; ++nt) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < PIECES; ++k) mma(z, a[y], pw[t][k][nt]);
+                for (int k = 0; k < PC; ++k) mma<F16>(z, a[y], pw[t][k][nt]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   if (lim(nt, i & 1) == mine) o[x * 2 + y][nt][i] += z[i];
@@ -698,26 +774,26 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
 
   // Row sums across the lanes, and (f) the factor of each column's accumulators.
   SA_DEVI void close(bool whole) {
+    float back = 1.f;
+    if constexpr (E4M3) {
+      // 2^(top - shift) as two factors: one would be below fp32's range for V rows near the
+      // smallest scale (2^-126), though the values are not
+      const int y = top == kNoLevel ? 0 : top - kShift16, h = y >> 1;
+      const float a = pow2(h);
+      back = pow2(y - h);
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[mt][nt][i] *= a;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         l[nt][k] = col_sum(l[nt][k]);
-        float x = 1.f;
-        if constexpr (E4M3) {
-          // 2^(mv - shift - m) as two factors: for V rows near the smallest scale (2^-126) the
-          // one would be flushed to zero, though the values are not
-          const float e = mv[nt][k] == -INFINITY ? -INFINITY : mv[nt][k] - kShift16 - ref_of(m[nt][k]);
-          const float a = ex2a(0.5f * e);
-          x = a;
-#pragma unroll
-          for (int mt = 0; mt < kMt; ++mt) {
-            o[mt][nt][k] *= a;
-            o[mt][nt][k + 2] *= a;
-          }
-        }
-        if (whole) x = l[nt][k] == 0.f ? 0.f : x / l[nt][k];
-        f[nt][k] = x;
+        f[nt][k] = !whole ? back : l[nt][k] == 0.f ? 0.f : back / l[nt][k];
       }
   }
   // fn(row, m, l) for the segment's rows.

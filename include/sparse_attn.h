@@ -476,9 +476,13 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  *            no initialisation; calls that may run at the same time need one each
  *   out      [B,Hq,T,d] contiguous, fp32 or bf16;  lse [B,Hq,T] fp32 or NULL
  * Logits, maxima, sums and accumulators are fp32; the weights enter their product with V in
- * 16-bit pieces that together keep 2^-11 (e4m3) or 2^-16 (bf16) of each for a bf16 output and
- * 2^-22 or better for fp32. The result is the same bit for bit from run to run on one kind of
- * device. One launch (one thread-block cluster per group of query rows) for few and short
+ * 16-bit pieces that together drop at most 2^-16 of each (bf16 rows, bf16 output), 2^-24 (bf16
+ * rows, fp32 output), 2^-11 (e4m3 rows, bf16 output) or 2^-22 (e4m3 rows, fp32 output). For
+ * e4m3 rows small weights are rounded to 2^-28 (bf16 output) or 2^-32 (fp32 output) of the
+ * row's largest instead, V rows whose scale is 2^140 below the largest attended one add
+ * nothing, and q . k over the codes, before the key's scale, times `scale` must not leave
+ * fp32's range. A logit of +infinity gives NaN in o and lse. The result is the same bit for
+ * bit from run to run on one kind of device. One launch (one thread-block cluster per group of query rows) for few and short
  * sequences, otherwise two (the second joins what CTAs share).
  */
 int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
