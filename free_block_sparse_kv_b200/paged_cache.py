@@ -199,7 +199,8 @@ def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, sca
     multiple of the cache's H: each kv head serves Hq / H query heads.
     ``kv_idx`` [B,H,cap] and ``kv_cnt`` [B,H] keep only the listed pages of each kv head, in
     the list format of :func:`attention.route` (its [B,H,1,cap] lists of one query block, with
-    block = page, are taken as they are). A row that attends nothing is 0, its lse -inf.
+    block = page, are taken as they are; a list may be empty, and cap may be 0). A row that
+    attends nothing is 0, its lse -inf.
     Returns ``out`` [B,Hq,T,d] (fp32, or bf16 by ``out_dtype``), and with ``return_lse`` also
     the fp32 log-sum-exp [B,Hq,T] of the scaled logits, by which partial results merge."""
     dt, dev, (P, H, page, d) = _check_cache(cache)
@@ -220,6 +221,8 @@ def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, sca
         cap = kv_idx.shape[-1]
         _ints("kv_idx", kv_idx, (B, H, cap), dev)
         _ints("kv_cnt", kv_cnt, (B, H), dev)
+        if cap == 0:
+            kv_idx = kv_cnt      # lists without room are not read, but an empty tensor has no address
     _flag(err_flag, dev)
     with _on(dev, stream):
         if out is None:

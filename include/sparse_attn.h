@@ -470,7 +470,8 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  *   kv_idx   [B,Hkv,cap] int32 and kv_cnt [B,Hkv]: kept logical pages of each kv head in
  *            the list format of routing (the lists of one query block, block = page;
  *            distinct entries). Entries outside [0, table_width) are ignored; kv_cnt is
- *            clamped to [0, cap]. Both NULL: every page
+ *            clamped to [0, cap]. With cap = 0 every list is empty and kv_idx is not read, but
+ *            is not NULL either. Both NULL: every page
  *   work     device scratch, 16-byte aligned, at least sparse_attn_decode_work_bytes(...)
  *            bytes for the current device (may be NULL when that is 0). Its contents need
  *            no initialisation; calls that may run at the same time need one each

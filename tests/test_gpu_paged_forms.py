@@ -1,0 +1,34 @@
+"""Decode and read calls at the edges of what they accept, and every form of the decode on the
+line of steps, against the fp64 oracle (tolerances as in test_gpu_paged_cache.py)."""
+import numpy as np
+import pytest
+import torch
+
+from free_block_sparse_kv_b200 import paged_cache as P
+from free_block_sparse_kv_b200 import sparse_attn as C
+from tests.test_gpu_paged_cache import BF16, E4M3, F32, _bf16, _check, _filled, _ints, _table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    C.load_library()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_lists_without_room(dtype):
+    """kv_idx [B,H,0]: every list is empty, every output 0 with lse -inf."""
+    rng = np.random.default_rng(1)
+    B, H, d, page = 3, 2, 64, 16
+    c = _filled(rng, 6, H, page, d, dtype)
+    q = _bf16(rng, B, 2 * H, 2, d)
+    table, lens = _ints([[0, 1], [2, 3], [4, 5]]), _ints([32, 0, 17])
+    for cnt in (0, 5):                               # clamped to the room
+        for idx, n in ((torch.zeros(B, H, 0, dtype=torch.int32, device="cuda"), _ints(np.full((B, H), cnt))),
+                       (torch.zeros(B, H, 1, 0, dtype=torch.int32, device="cuda"), _ints(np.full((B, H, 1), cnt)))):
+            out, lse = P.decode(q, c, table, lens, idx, n, return_lse=True,
+                                out=torch.full((B, 2 * H, 2, d), 7.0, device="cuda"))
+            assert not out.any() and torch.isneginf(lse).all()
