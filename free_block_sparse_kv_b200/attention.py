@@ -409,13 +409,19 @@ class BlockSparseAttention:
 
     def check(self):
         """Raise if an earlier call failed on the device (synchronises): SA_ERR_RANGE when a
-        pooled fp16 table value did not fit (the output is then not valid), SA_ERR_TIMEOUT
-        when a bounded device wait gave up. The flag is sticky: it stays set until cleared
+        pooled fp16 table value did not fit (the output is then not valid), SA_ERR_INDEX when
+        a paged-cache call that shares the flag met a page number, length or position out of
+        range (a forward that finds the flag set skips its work), SA_ERR_TIMEOUT when a
+        bounded device wait gave up. The flag is sticky: it stays set until cleared
         with ``err_flag.zero_()``."""
         flag = int(self.err_flag.item())
         if flag & C.SA_FLAG_RANGE:
             raise C.SparseAttnError(C.SA_ERR_RANGE, "a pooled fp16 table value (V copy, value "
                                     "sum or M_j) does not fit in fp16 (|x| >= 65520); scale V "
                                     f"down by a power of two (flag {flag:#x})")
+        if flag & C.SA_FLAG_INDEX:
+            raise C.SparseAttnError(C.SA_ERR_INDEX, "a paged-cache call with this flag met a page "
+                                    "number, length or position out of range, and forwards skip "
+                                    f"their work while the flag is set (flag {flag:#x})")
         if flag:
             raise C.SparseAttnError(C.SA_ERR_TIMEOUT, f"device wait timed out (flag {flag:#x})")

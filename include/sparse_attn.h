@@ -57,8 +57,9 @@ enum {
 };
 
 /* Bit set in err_flag by the pool when a value of its fp16 outputs (V copy, value sums,
- * M_j) would round to infinity (|x| >= 65520). The other bits of err_flag mark bounded
- * device waits that gave up (SA_ERR_TIMEOUT). */
+ * M_j) would round to infinity (|x| >= 65520). The bits below it mark bounded
+ * device waits that gave up (SA_ERR_TIMEOUT). A forward that finds any bit set, SA_FLAG_INDEX
+ * among them, skips its work. */
 #define SA_FLAG_RANGE (1 << 20)
 
 /* Bit set in err_flag by the paged-cache entry points when a page number, a length or a
@@ -349,7 +350,8 @@ int sparse_attn_wait_selftest(int32_t* err_flag, int rounds, int32_t* waited, vo
  *                     after that find the flag set and skip their work. The call
  *                     itself still returns SA_OK (the kernel runs asynchronously):
  *                     a non-zero flag after the stream completes means
- *                     SA_ERR_TIMEOUT and the output is not valid. The flag is
+ *                     SA_ERR_TIMEOUT (or what its SA_FLAG_ bits say, from the
+ *                     call that set them) and the output is not valid. The flag is
  *                     sticky: clear it before the next call.
  * Ranges: probabilities enter the value products as fp16 at most 2^11 (relative to the
  * row's running maximum); with order 1 the operand scale * alpha * q_t is fp16 too, and
