@@ -134,11 +134,11 @@ def _on(device, stream):
 
 def _apart(name, x):
     """Rows of a destination must not share memory."""
-    need = x.shape[3]
+    need = x.shape[3] if x.numel() else 0     # elements from the first to the last of what is nested
     for st, n in sorted((x.stride(i), x.shape[i]) for i in range(3) if x.shape[i] > 1):
         if st < need:
             raise ValueError(f"the rows of {name} overlap")
-        need = st * n
+        need += st * (n - 1)
 
 
 def cache_append(cache: PagedCache, k, v, page_table, start, count=None, err_flag=None, stream=None):

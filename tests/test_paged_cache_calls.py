@@ -25,3 +25,28 @@ def test_flag_of_the_block_sparse_call(flag, code):
     op.err_flag.zero_()
     op.check()
     P.check(op.err_flag)
+
+
+def test_destinations_whose_rows_do_not_overlap():
+    """Every second row (or head) of a buffer with an odd number of them is a destination; the
+    exact check is against the addresses themselves."""
+    def overlaps(x):
+        b, h, t = torch.meshgrid(*(torch.arange(n) for n in x.shape[:3]), indexing="ij")
+        sb, sh, st, _ = x.stride()
+        at = (b * sb + h * sh + t * st).reshape(-1).sort().values
+        return bool((at.diff() < x.shape[3]).any())
+
+    y = torch.zeros(3, 5, 7, 64, dtype=torch.bfloat16)
+    fine = [y[:, :, ::2], y[:, ::2], y[::2, ::2, ::2], y[:, :, ::3], y.transpose(1, 2)[:, ::2],
+            torch.zeros(2, 7, 3, 5, 64, dtype=torch.bfloat16)[:, :, 1].transpose(1, 2),
+            y[:1, :, 1::2],
+            y[:, :, :0], y[:0], y[:, :, 3:4]]
+    for x in fine:
+        assert not overlaps(x)
+        P._apart("k", x)
+    bad = [y[:1].expand(2, 5, 7, 64), torch.as_strided(y, (2, 3, 8, 64), (64, 512, 64, 1)),
+           torch.as_strided(y, (1, 3, 4, 64), (0, 192, 64, 1)), torch.as_strided(y, (1, 1, 4, 64), (0, 0, 56, 1))]
+    for x in bad:
+        assert overlaps(x)
+        with pytest.raises(ValueError, match="overlap"):
+            P._apart("k", x)
