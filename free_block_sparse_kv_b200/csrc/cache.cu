@@ -266,7 +266,7 @@ cudaError_t append_t(const CacheAppendArgs& p, cudaStream_t st) {
 template <int D, bool E4M3>
 cudaError_t read_t(const CacheReadArgs& p, cudaStream_t st) {
   constexpr int per = kThreads / (D / 8) * kReadUnroll;
-  const long long bh = (long long)p.B * p.c.H, tiles = (p.N + per - 1) / per;
+  const long long bh = (long long)p.B * p.c.H, tiles = ((long long)p.N + per - 1) / per;
   const long long share = (kReadBlocks + bh - 1) / bh;
   const dim3 grid((unsigned)std::min(tiles, share), (unsigned)p.c.H, (unsigned)p.B);
   cache_read_kernel<D, E4M3><<<grid, kThreads, 0, st>>>(p);

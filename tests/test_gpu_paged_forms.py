@@ -32,3 +32,21 @@ def test_lists_without_room(dtype):
             out, lse = P.decode(q, c, table, lens, idx, n, return_lse=True,
                                 out=torch.full((B, 2 * H, 2, d), 7.0, device="cuda"))
             assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_read_into_far_more_rows_than_there_are():
+    """N is the destination's room, not what is read: up to 2^31 - 1."""
+    rng = np.random.default_rng(2)
+    H, d, page, n = 2, 64, 16, 21
+    for dtype in (BF16, E4M3):
+        c = _filled(rng, 2, H, page, d, dtype)
+        table, lens = _ints([[1, 0]]), _ints([n])
+        want = torch.zeros(2, 1, H, n, d, dtype=BF16, device="cuda")
+        P.cache_read(c, table, lens, want[0], want[1])
+        got = torch.zeros_like(want)
+        C.sparse_attn_cache_read(c.k, c.v, c.k_scale, c.v_scale,
+                                 C.SA_CACHE_BF16 if dtype == BF16 else C.SA_CACHE_E4M3, 2, page, table, 2,
+                                 2, None, lens, 1, H, (1 << 31) - 1, d, got[0], got[1],
+                                 (0, n * d, d), (0, n * d, d), None,
+                                 torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(got, want)
