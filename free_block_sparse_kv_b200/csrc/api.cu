@@ -1,6 +1,7 @@
 // C ABI of the library: argument checks on the host, then one kernel launch per
 // entry point on the caller's stream. No allocation, no synchronisation.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -130,16 +131,15 @@ int check_decode_shape(int B, int Hq, int Hkv, int T, int d) {
 }
 
 int sm_count(int* sms) {
-  static int cache[64];
+  static std::atomic<int> cache[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && dev >= 0 && dev < 64 && cache[dev] > 0) {
-    *sms = cache[dev];
+  if (e == cudaSuccess && dev >= 0 && dev < 64 &&
+      (*sms = cache[dev].load(std::memory_order_relaxed)) > 0)
     return SA_OK;
-  }
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(SA_ERR_LAUNCH, "SM count: %s", cudaGetErrorString(e));
-  if (dev >= 0 && dev < 64) cache[dev] = *sms;
+  if (dev >= 0 && dev < 64) cache[dev].store(*sms, std::memory_order_relaxed);
   return SA_OK;
 }
 

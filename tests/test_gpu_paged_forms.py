@@ -50,3 +50,36 @@ def test_read_into_far_more_rows_than_there_are():
                                  (0, n * d, d), (0, n * d, d), None,
                                  torch.cuda.current_stream().cuda_stream)
         assert torch.equal(got, want)
+
+
+def test_calls_from_several_threads():
+    """Decodes of different shapes from eight host threads at once, each on a stream of its own,
+    give what they give one after the other."""
+    import threading
+    rng = np.random.default_rng(5)
+    page, d, jobs = 32, 64, []
+    for i in range(8):
+        B, H, G, dtype = 1 + i % 3, 2, (1, 10, 20)[i % 3], (BF16, E4M3)[i % 2]
+        lens = [int(x) for x in rng.integers(1, 3000, B)]
+        num = sum(-(-n // page) for n in lens)
+        table = _ints(_table(rng, lens, page, num, spare=3000 * (i // 4)))
+        jobs.append((_bf16(rng, B, G * H, 1, d), _filled(rng, num, H, page, d, dtype), table, _ints(lens)))
+    want = [P.decode(*j, return_lse=True) for j in jobs]
+    torch.cuda.synchronize()
+    P._work_bytes.cache_clear()
+    got, go = [None] * 8, threading.Barrier(8)
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        go.wait(timeout=60)
+        for _ in range(20):
+            got[i] = P.decode(*jobs[i], return_lse=True, stream=stream)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    for (o, l), (o2, l2) in zip(want, got):
+        assert torch.equal(o, o2) and torch.equal(l, l2)
