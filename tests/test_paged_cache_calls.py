@@ -50,3 +50,16 @@ def test_destinations_whose_rows_do_not_overlap():
         assert overlaps(x)
         with pytest.raises(ValueError, match="overlap"):
             P._apart("k", x)
+
+
+def test_addresses_of_integer_types():
+    """Every entry point takes device addresses as integers, subclasses of int among them."""
+    class Address(int):
+        pass
+
+    t = torch.zeros(3)
+    assert C._ptr(Address(64)) == 64 and C._ptr(64) == 64 and C._ptr(None) is None
+    assert C._ptr(t) == t.data_ptr()
+    C.sparse_attn_cache_append(Address(0), Address(0), (0, 0, 0), (0, 0, 0), 0, 1, 1, 64, Address(0), 1, 1,
+                               Address(0), None, Address(0), Address(0), None, None, C.SA_CACHE_BF16, 1, 16,
+                               None, Address(0))
