@@ -83,3 +83,76 @@ def test_calls_from_several_threads():
         t.join(timeout=120)
     for (o, l), (o2, l2) in zip(want, got):
         assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+# ------------------------------------------------------------------ every form on the line of steps
+LINE = [  # B, Hq, H, T, d, page, lens: 9-16, 17-32 and more rows of a kv head
+    (70, 36, 3, 1, 128, 32, [1 + (37 * b * b) % 700 for b in range(70)]),
+    (90, 16, 1, 1, 64, 16, [(b * 53) % 1900 if b % 7 else 0 for b in range(90)]),
+    (40, 60, 3, 1, 128, 16, [1 + (61 * b * b) % 900 for b in range(40)]),
+    (80, 4, 1, 5, 64, 64, [(29 * b) % 1500 + (b % 3) for b in range(80)]),
+    (40, 40, 1, 1, 128, 64, [5 + (41 * b * b) % 1100 for b in range(40)]),
+    (12, 16, 2, 16, 64, 32, [16 * b + 3 if b % 4 else 2500 + b for b in range(12)]),
+    (33, 9, 9, 11, 128, 128, [(b * 97) % 1300 for b in range(33)]),
+    # more sequences than a warp scans by itself, 20 rows each
+    (300, 20, 1, 1, 64, 16, [(11 * b) % 200 for b in range(300)]),
+    # several short segments to a warp's share
+    (1500, 20, 2, 1, 128, 16, [(7 * b) % 61 for b in range(1500)]),
+    (1200, 40, 2, 1, 128, 16, [(11 * b) % 67 for b in range(1200)]),
+    (700, 40, 1, 2, 64, 32, [(13 * b) % 230 for b in range(700)]),
+    # a few long segments: whole CTAs for each, CTAs left over
+    (1, 3, 3, 1, 128, 64, [40001]),
+    (5, 4, 1, 3, 128, 64, [20000, 20011, 19990, 0, 20003]),
+    (3, 24, 3, 2, 64, 128, [21000, 21004, 20998]),
+    (2, 20, 2, 4, 128, 32, [9003, 9100]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(LINE)))
+def test_line(case, out_dtype, dtype):
+    """Shares that hold parts of several segments, whole CTAs for a few long ones, row groups
+    that read the same keys. A table wider than the lengths keeps the call off the clusters."""
+    B, Hq, H, T, d, page, lens = LINE[case]
+    rng = np.random.default_rng(100 + case)
+    num = sum(-(-n // page) for n in lens) + 1
+    table = _table(rng, lens, page, num, spare=60000 // page)
+    code = C.SA_CACHE_BF16 if dtype == BF16 else C.SA_CACHE_E4M3
+    odt = C.SA_OUT_F32 if out_dtype == F32 else C.SA_OUT_BF16
+    assert C.sparse_attn_decode_work_bytes(B, Hq, H, T, d, code, page, table.shape[1], -1, odt) > 0
+    c = _filled(rng, num, H, page, d, dtype)
+    q = _bf16(rng, B, Hq, T, d)
+    flag = _ints([0])
+    out, lse = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype, return_lse=True,
+                        err_flag=flag)
+    P.check(flag)
+    _check(out, lse, out_dtype, d, 1 / np.sqrt(d), q, c, table, lens, page)
+    again = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("B,Hq,H,T,d,page,lens,cap", [
+    (30, 24, 2, 1, 128, 32, [(b * 71) % 1400 for b in range(30)], 30),
+    (20, 60, 3, 1, 64, 16, [(b * 113) % 1500 for b in range(20)], 90),
+    (24, 12, 2, 6, 128, 64, [(b * 89) % 1300 for b in range(24)], 20)])
+def test_line_kept_pages(B, Hq, H, T, d, page, lens, cap, dtype):
+    rng = np.random.default_rng(cap)
+    num = sum(-(-n // page) for n in lens) + 1
+    table = _table(rng, lens, page, num, spare=3)
+    c = _filled(rng, num, H, page, d, dtype)
+    q = _bf16(rng, B, Hq, T, d)
+    wide = cap + 40000 // page                       # lists with much room: off the clusters
+    idx, cnt = np.full((B, H, wide), -1), np.zeros((B, H), int)
+    kept = [[[] for _ in range(H)] for _ in range(B)]
+    for b in range(B):
+        pages = -(-lens[b] // page)
+        for h in range(H):
+            m = int(rng.integers(0, min(cap, pages) + 1))
+            kept[b][h] = sorted(rng.choice(pages, m, replace=False).tolist()) if m else []
+            idx[b, h, :m], cnt[b, h] = kept[b][h], m
+    code = C.SA_CACHE_BF16 if dtype == BF16 else C.SA_CACHE_E4M3
+    assert C.sparse_attn_decode_work_bytes(B, Hq, H, T, d, code, page, table.shape[1], wide) > 0
+    out, lse = P.decode(q, c, _ints(table), _ints(lens), _ints(idx), _ints(cnt), return_lse=True)
+    _check(out, lse, F32, d, 1 / np.sqrt(d), q, c, table, lens, page, kept)
