@@ -57,12 +57,14 @@ namespace {
 
 constexpr int kLaneUnits = 8;          // units of a lane where a warp scans them by itself
 // A cluster per segment saves the scan, the partials' way through memory and the second
-// kernel: 5 us, about as long as this many steps of a warp take (1.3 us each when all SMs
-// load). With 100 kept pages of 64 rows in each of 64 heads (17 steps in clusters of two, 15
-// on the line) it takes 40 us against 45. Longer ones run on the line, which their lengths
-// cannot unbalance (64 heads of 100 to 32,000 rows: 84 us against 95), but for one sequence
-// alone: 16 heads x 32,000 rows 48 us in clusters of four, 51 on the line.
+// kernel: 3 to 5 us, the time of about this many steps of a warp. Equal lengths, 64 heads: 4,000
+// bf16 rows 26.0 us against 29.9 on the line, 8,000 44.9 against 49.0; 48 heads (a third of the
+// SMs idle) 8,000 rows 34.3 against 38.9, but 8-bit rows no faster from 16,000 on and 32 query
+// rows slower from 4,000 on (37.6 against 35.3).
 constexpr long long kClusterSlack = 4;
+// Longer shares run on the line, which uneven lengths cannot unbalance: 64 heads of 1 to 16,000
+// 8-bit rows 41.8 us in clusters, 33.9 on the line; 64 of 16,000 bf16 rows each 83.1 and 87.2.
+constexpr long long kClusterSteps = 32;
 constexpr int kNoPos = 0x7FFFFF00;     // position of keys that nothing attends
 // The level that a column's weights are relative to is set this far (base 2) above the running
 // maximum when that passes it: most steps then rescale nothing.
@@ -220,6 +222,7 @@ struct Math : Layout<D, E4M3, WARPS, STAGES> {
   // there, and the steps added to nearest here: 4 x 16 heads x 63,960 bf16 rows 302 us against
   // 300, 40 heads x 75,600 e4m3 rows 131 against 125, 32 bf16 rows a segment 48.2 against 46.0.
   static constexpr bool kAdds = F32;
+  static constexpr bool kF32 = F32;
   static constexpr int kRows = 8 * NT, kMt = D / 16;
   // With 32 rows the queries would take 64 registers of a lane: they stay in shared memory.
   static constexpr bool kQs = NT == 4;
@@ -1510,6 +1513,13 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   // steps of a segment whose table row (or list) is full
   const long long most =
       (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) + M::kKeys - 1) / M::kKeys;
+  // CTAs of the line: up to eight query rows, eight SMs in nine. 132 CTAs against 148, as
+  // measured (three calls on one kind of card): 4 x 16 heads x 63,960 bf16 rows 299 us against
+  // 315, as e4m3 rows 159 against 174; 40 heads x 75,600 e4m3 rows 126 against 133; 64 ragged
+  // bf16 sequences 167 against 173, e4m3 101 against 100; 64 x 8 heads x 1,500 e4m3 rows, fp32
+  // out, 45.4 against 44.5. On another B200, where the first takes 325 us, 148 CTAs took 321.
+  // More query rows need every SM (32 rows a segment, 8 x 8 heads x 16,000: 116 against 112).
+  const int line = M::kRows <= 8 ? p.sms - p.sms / 9 : p.sms;
   cfg.blockDim = dim3(M::kThreads);
   cfg.dynamicSmemBytes = M::smem(true);
   cfg.attrs = &attr;
@@ -1519,14 +1529,23 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   // work as the line would: see kClusterSlack.
   int size = 8;
   while (size > 1 && segs * size > p.sms) size /= 2;
-  const long long on_line = (segs * most + (long long)p.sms * M::kWarps - 1) / ((long long)p.sms * M::kWarps);
+  const long long on_line = (segs * most + (long long)line * M::kWarps - 1) / ((long long)line * M::kWarps);
   for (; size >= 1 && segs * size <= p.sms; size /= 2) {
     const long long in_cluster = (most + size * M::kWarps - 1) / (size * M::kWarps);
-    // one sequence's heads are equally long, and 64 SMs come close to what HBM gives bf16 rows
-    // of up to eight queries; 8-bit rows and more queries need the SMs' own rate
-    const bool even = p.B == 1 && !p.kv_idx &&
-                      segs * size * (M::kE4M3 || M::kRows > 8 ? 12 : 24) >= 10ll * p.sms;
-    if (in_cluster > on_line + kClusterSlack && !even) break;
+    // One sequence's heads are equally long, and clusters keep up with HBM over bf16 rows of up
+    // to eight queries where they hold enough SMs: 28 heads x 75,600 rows 157 us (112 CTAs)
+    // against 164 on the line, 20 x 32,000 52.9 (80) against 57.7, 18 x 40,000 59.5 (144) against
+    // 62.6; with 64 CTAs 16 x 32,000 45.6 against 47.5, but 32 x 75,600 191 against 183. fp32
+    // outputs take more of an SM: 112 CTAs 158 us against 166, 144 69.7 against 64.9, 64 57.1
+    // against 49.0. 32 heads x 32,000 rows x 16 queries 90.5 (128) against 93.2. 8-bit rows: no
+    // difference in 20 shapes.
+    const long long held = segs * size;
+    const bool enough = M::kRows > 8 ? 6 * held >= 5ll * p.sms
+                        : M::kF32    ? 8 * held >= 5ll * p.sms && held <= line
+                                     : 9 * held >= 4ll * p.sms ||
+                                           (12 * held >= 5ll * p.sms && in_cluster <= 2 * kClusterSteps);
+    const bool even = p.B == 1 && !p.kv_idx && !M::kE4M3 && enough;
+    if ((in_cluster > on_line + kClusterSlack || in_cluster > kClusterSteps) && !even) break;
     auto* kern = decode_kernel<D, M, true>;
     cudaError_t e = allow_smem(kern, M::smem(true), ready_cluster);
     if (e != cudaSuccess) return e;
@@ -1543,14 +1562,8 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
     pl.size = size;
     return cudaSuccess;
   }
-  // Up to eight query rows HBM is the bound, and eight SMs in nine ask for as much as it gives;
-  // 132 CTAs against 148, inputs of three calls in turn: 4 x 16 heads x 63,960 bf16 rows 304 us
-  // against 320 (on another B200 325 against 321), 40 heads x 75,600 e4m3 rows 131 against 134,
-  // 64 ragged e4m3 sequences 106 against 104. More rows need every SM (32 rows a segment, 8 x 8
-  // heads x 16,000: 116 against 112). And never more CTAs than full tables give every warp a
-  // step.
-  const int sms = M::kRows <= 8 ? p.sms - p.sms / 9 : p.sms;
-  pl.ctas = (int)std::min<long long>(sms, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
+  // Never more CTAs than full tables give every warp a step.
+  pl.ctas = (int)std::min<long long>(line, (segs * std::max(most, 1ll) + M::kWarps - 1) / M::kWarps);
   pl.bytes = (size_t)pl.ctas * (sizeof(Record) + (M::kWarps + 2) * (size_t)M::kRows * (D + 2) * 4);
   return allow_smem(decode_kernel<D, M, false>, M::smem(false), ready_line);
 }

@@ -132,6 +132,27 @@ def test_line(case, out_dtype, dtype):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("out_dtype,Hq,H,T,d,n,spare", [
+    (BF16, 9, 9, 1, 128, 3001, 90000), (BF16, 20, 10, 1, 64, 2500, 90000), (BF16, 14, 14, 3, 128, 17, 90000),
+    (BF16, 16, 16, 1, 128, 30001, 100), (F32, 24, 24, 1, 128, 1501, 90000), (F32, 28, 14, 4, 64, 2000, 90000),
+    (BF16, 288, 32, 1, 128, 700, 60000), (F32, 34, 34, 11, 64, 650, 60000), (BF16, 66, 33, 12, 128, 333, 60000)])
+def test_heads_of_one_sequence_in_clusters(out_dtype, Hq, H, T, d, n, spare):
+    """bf16 rows of one sequence whose heads hold most SMs: a cluster each, at any length. (More
+    than 31 clusters of four CTAs need not fit at once, which the device says: 34 did not, and
+    run on the line.)"""
+    rng = np.random.default_rng(H)
+    page, lens = 64, [n]
+    num = -(-n // page) + 1
+    table = _table(rng, lens, page, num, spare=spare // page)
+    odt = C.SA_OUT_F32 if out_dtype == F32 else C.SA_OUT_BF16
+    if H <= 31:
+        assert C.sparse_attn_decode_work_bytes(1, Hq, H, T, d, C.SA_CACHE_BF16, page, table.shape[1], -1, odt) == 0
+    c = _filled(rng, num, H, page, d, BF16)
+    q = _bf16(rng, 1, Hq, T, d)
+    out, lse = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype, return_lse=True)
+    _check(out, lse, out_dtype, d, 1 / np.sqrt(d), q, c, table, lens, page)
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("B,Hq,H,T,d,page,lens,cap", [
     (30, 24, 2, 1, 128, 32, [(b * 71) % 1400 for b in range(30)], 30),
