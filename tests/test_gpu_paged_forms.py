@@ -6,7 +6,9 @@ import torch
 
 from free_block_sparse_kv_b200 import paged_cache as P
 from free_block_sparse_kv_b200 import sparse_attn as C
-from tests.test_gpu_paged_cache import BF16, E4M3, F32, _bf16, _check, _filled, _ints, _table
+from oracle import paged_cache as O
+from tests.test_gpu_paged_cache import (BF16, E4M3, F32, _bf16, _bounds, _check, _filled, _ints, _np,
+                                        _table)
 
 pytestmark = pytest.mark.gpu
 
@@ -109,9 +111,8 @@ LINE = [  # B, Hq, H, T, d, page, lens: 9-16, 17-32 and more rows of a kv head
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
-@pytest.mark.parametrize("out_dtype", [F32, BF16])
 @pytest.mark.parametrize("case", range(len(LINE)))
-def test_line(case, out_dtype, dtype):
+def test_line(case, dtype):
     """Shares that hold parts of several segments, whole CTAs for a few long ones, row groups
     that read the same keys. A table wider than the lengths keeps the call off the clusters."""
     B, Hq, H, T, d, page, lens = LINE[case]
@@ -119,17 +120,23 @@ def test_line(case, out_dtype, dtype):
     num = sum(-(-n // page) for n in lens) + 1
     table = _table(rng, lens, page, num, spare=60000 // page)
     code = C.SA_CACHE_BF16 if dtype == BF16 else C.SA_CACHE_E4M3
-    odt = C.SA_OUT_F32 if out_dtype == F32 else C.SA_OUT_BF16
-    assert C.sparse_attn_decode_work_bytes(B, Hq, H, T, d, code, page, table.shape[1], -1, odt) > 0
     c = _filled(rng, num, H, page, d, dtype)
     q = _bf16(rng, B, Hq, T, d)
-    flag = _ints([0])
-    out, lse = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype, return_lse=True,
-                        err_flag=flag)
-    P.check(flag)
-    _check(out, lse, out_dtype, d, 1 / np.sqrt(d), q, c, table, lens, page)
-    again = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype)
-    assert torch.equal(out, again)
+    ks, vs = (None if x is None else _np(x) for x in (c.k_scale, c.v_scale))
+    scale = 1 / np.sqrt(d)
+    want, lse, vmax, qk = O.decode(_np(q), _np(c.k), _np(c.v), ks, vs, table, lens, page, scale)
+    empty = np.isneginf(lse)
+    for out_dtype, odt in ((F32, C.SA_OUT_F32), (BF16, C.SA_OUT_BF16)):
+        assert C.sparse_attn_decode_work_bytes(B, Hq, H, T, d, code, page, table.shape[1], -1, odt) > 0
+        flag = _ints([0])
+        out, got_lse = P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype, return_lse=True,
+                                err_flag=flag)
+        P.check(flag)
+        tol, ltol = _bounds(dtype, out_dtype, d, scale, want, lse, vmax, qk)
+        assert (np.abs(_np(out) - want) <= tol).all()
+        assert np.array_equal(np.isneginf(_np(got_lse)), empty) and not _np(out)[empty].any()
+        assert (np.abs(_np(got_lse)[~empty] - lse[~empty]) <= ltol[~empty]).all()
+        assert torch.equal(out, P.decode(q, c, _ints(table), _ints(lens), out_dtype=out_dtype))
 
 
 @pytest.mark.parametrize("out_dtype,Hq,H,T,d,n,spare", [
