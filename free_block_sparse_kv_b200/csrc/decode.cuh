@@ -19,7 +19,7 @@
 //    leave (m, l, numerator) partials, joined first inside the CTA and then, for segments
 //    that span CTAs, by a second small kernel. Orders are fixed: same bits every run.
 //  - Where one cluster per segment fills the GPU about as well (few, short segments), that
-//    takes one launch and no scan: 16 heads of 1,560 rows 10.4 us against 12.4 on the line.
+//    takes one launch and no scan: 16 heads of 1,560 rows 8.6 us against 10.5 on the line.
 //  - Products run on mma.sync with the keys as the M dimension (S^T = K Q^T, O^T = V^T P^T):
 //    one query row wastes 7/8 of a tile, not 15/16, and the tensor work (2 cycles of an SM a
 //    product) stays below the time of the loads up to R = 16. At R = 32 it is about half of
@@ -27,10 +27,10 @@
 //    would move that.
 //  - Twelve warps of two stages where eight rows suffice, eight of three or two otherwise
 //    (registers): 64 ragged e4m3 sequences 108 us against 121 with eight warps of three.
-// Measured on three B200s (calls back to back, inputs of three in turn): 4 x 16 heads x 63,960
-// bf16 rows 298-325 us (7.0-6.4 TB/s); 40 heads x 75,600 e4m3 rows 126-132 us (6.2-5.9 TB/s);
-// 64 e4m3 sequences of 0 to 8,191 rows, 8 kv heads of 4 query heads, pages of 16: 101-106 us
-// (5.4-5.2 TB/s).
+// Measured on several B200s (calls back to back, inputs of three in turn): 4 x 16 heads x 63,960
+// bf16 rows 298-325 us (7.0-6.4 TB/s); 40 heads x 75,600 e4m3 rows 125-133 us (6.2-5.9 TB/s),
+// 130 with an fp32 output where it is 126; 64 e4m3 sequences of 0 to 8,191 rows, 8 kv heads of 4 query heads,
+// pages of 16: 100-108 us (5.5-5.1 TB/s).
 //
 // Roundings below fp32. P enters its product as 16-bit pieces, each the rest of the one
 // before: as many as keep the dropped rest below the output's own rounding (Math::PIECES).
@@ -57,7 +57,8 @@ namespace {
 
 constexpr int kLaneUnits = 8;          // units of a lane where a warp scans them by itself
 // A cluster per segment saves the scan, the partials' way through memory and the second
-// kernel: 3 to 5 us, the time of about this many steps of a warp. Equal lengths, 64 heads: 4,000
+// kernel: 2 to 5 us, the time of about this many steps of a warp. 100 kept pages of 64 rows in
+// each of 64 heads: 38.6 us against 42.8 on the line. Equal lengths, 64 heads: 4,000
 // bf16 rows 26.0 us against 29.9 on the line, 8,000 44.9 against 49.0; 48 heads (a third of the
 // SMs idle) 8,000 rows 34.3 against 38.9, but 8-bit rows no faster from 16,000 on and 32 query
 // rows slower from 4,000 on (37.6 against 35.3).
@@ -1004,7 +1005,7 @@ __global__ void __launch_bounds__(M::kThreads, 1) decode_kernel(DecodeArgs p, in
     ctas = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
     // Few long segments: whole CTAs for each, where that lengthens no share by more than 1/32,
     // spares the CTAs that would hold the end of one segment and the start of another (they
-    // took 15,000 cycles longer: four segments of 32 rows 52 us, so cut 47 us).
+    // took 15,000 cycles longer: four segments of 32 rows 53.2 us, so cut 48.7 us).
     bool aligned = per == 1 && by_warp && total > 0 && total < (1ll << 32) && ctas == (int)gridDim.x;
     int k = 0;                            // CTAs of each segment of this lane's unit
     if (aligned) {
@@ -1514,10 +1515,11 @@ cudaError_t plan(const DecodeArgs& p, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   const long long most =
       (((long long)(p.kv_idx ? p.cap : p.c.table_width) << p.c.page_log2) + M::kKeys - 1) / M::kKeys;
   // CTAs of the line: up to eight query rows, eight SMs in nine. 132 CTAs against 148, as
-  // measured (three calls on one kind of card): 4 x 16 heads x 63,960 bf16 rows 299 us against
-  // 315, as e4m3 rows 159 against 174; 40 heads x 75,600 e4m3 rows 126 against 133; 64 ragged
-  // bf16 sequences 167 against 173, e4m3 101 against 100; 64 x 8 heads x 1,500 e4m3 rows, fp32
-  // out, 45.4 against 44.5. On another B200, where the first takes 325 us, 148 CTAs took 321.
+  // measured (two B200s): 4 x 16 heads x 63,960 bf16 rows 299 and 306 us against 315 and 326, as
+  // e4m3 rows 159 against 174; 40 heads x 75,600 e4m3 rows 126 and 130 against 133 and 134; 64
+  // ragged bf16 sequences 167 against 173, e4m3 102 and 105 against 102 and 103; 64 x 8 heads x
+  // 1,500 e4m3 rows, fp32 out, 45.4 against 44.5. On a third, where the first takes 325 us, 148
+  // CTAs took 321.
   // More query rows need every SM (32 rows a segment, 8 x 8 heads x 16,000: 116 against 112).
   const int line = M::kRows <= 8 ? p.sms - p.sms / 9 : p.sms;
   cfg.blockDim = dim3(M::kThreads);

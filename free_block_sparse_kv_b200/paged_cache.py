@@ -6,7 +6,8 @@ The caller owns the page tables and the lengths (int32 device tensors) and decid
 pages a sequence holds; torch provides memory and the stream, every step is one call into
 ``libsparse_attn.so``. Calls may name another stream than the current one (``stream=``) and
 tensors of another device than the current one: buffers that a call makes belong to the
-stream and the device that it runs on.
+stream and the device that it runs on. As for every call on a stream of its own, the caller
+orders it behind what made the inputs and keeps them until it is done.
 
     cache = allocate_cache(num_pages, H, page=64, d=128, dtype=torch.float8_e4m3fn)
     cache_append(cache, k, v, page_table, start)          # k, v: [B,H,T,d] bf16 rows
@@ -199,8 +200,9 @@ def decode(q, cache: PagedCache, page_table, lens, kv_idx=None, kv_cnt=None, sca
     multiple of the cache's H: each kv head serves Hq / H query heads.
     ``kv_idx`` [B,H,cap] and ``kv_cnt`` [B,H] keep only the listed pages of each kv head, in
     the list format of :func:`attention.route` (its [B,H,1,cap] lists of one query block, with
-    block = page, are taken as they are; a list may be empty, and cap may be 0). A row that
-    attends nothing is 0, its lse -inf.
+    block = page, are taken as they are; a list may be empty, and cap may be 0). Routing lists per
+    query head: where Hq > H the caller joins the lists of a kv head's group. A row that attends
+    nothing is 0, its lse -inf. Tables and lists no wider than needed run short sequences faster.
     Returns ``out`` [B,Hq,T,d] (fp32, or bf16 by ``out_dtype``), and with ``return_lse`` also
     the fp32 log-sum-exp [B,Hq,T] of the scaled logits, by which partial results merge."""
     dt, dev, (P, H, page, d) = _check_cache(cache)

@@ -485,8 +485,11 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  * row's largest instead, V rows whose scale is 2^140 below the largest attended one add
  * nothing, and q . k over the codes, before the key's scale, times `scale` must not leave
  * fp32's range. A logit of +infinity gives NaN in o and lse. The result is the same bit for
- * bit from run to run on one kind of device. One launch (one thread-block cluster per group of query rows) for few and short
- * sequences, otherwise two (the second joins what CTAs share).
+ * bit from run to run on one kind of device. One launch (one thread-block cluster per group of
+ * query rows) for few and short sequences, otherwise two (the second joins what CTAs share). The
+ * host decides by table_width (or cap), as the lengths are on the device: a table much wider
+ * than they need costs short sequences 2 to 5 microseconds. More than 32 query rows of a kv head, (Hq / Hkv) * T, read its
+ * keys once per 32.
  */
 int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
                        int Hkv, int T, int d, const void* k_pages, const void* v_pages,
