@@ -425,8 +425,9 @@ int sparse_attn_forward_split_plan(int B, int H, int Nq, int Nk, int d, int bloc
  *                     is outside [0, T], a start or first row is negative, or an appended
  *                     position is past table_width * page. Rows without a valid place are
  *                     left out (not written, not attended). Sticky, like every err_flag.
- * B * H <= 65535; B * Hq * T, table_width * page and cap * page <= 2^30; pointers 16-byte aligned, int32 arrays and lse 4-byte
- * aligned, scales 16-byte aligned. Nothing is allocated; one stream; graph capture is fine.
+ * B * H <= 65535; B * Hq * T, table_width * page and cap * page <= 2^30; pointers 16-byte
+ * aligned, int32 arrays and lse 4-byte aligned, scales 16-byte aligned. Nothing is allocated;
+ * one stream; graph capture is fine.
  *
  * sparse_attn_cache_append: token t < count[b] of sequence b (k, v [B,H,T,d] bf16) is
  * written at position start[b] + t. For SA_CACHE_E4M3 each row is quantised as it is
@@ -488,8 +489,8 @@ int sparse_attn_cache_read(const void* k_pages, const void* v_pages, const uint8
  * bit from run to run on one kind of device. One launch (one thread-block cluster per group of
  * query rows) for few and short sequences, otherwise two (the second joins what CTAs share). The
  * host decides by table_width (or cap), as the lengths are on the device: a table much wider
- * than they need costs short sequences 2 to 5 microseconds. More than 32 query rows of a kv head, (Hq / Hkv) * T, read its
- * keys once per 32.
+ * than they need costs short sequences 2 to 5 microseconds. More than 32 query rows of a kv
+ * head, (Hq / Hkv) * T, read its keys once per 32.
  */
 int sparse_attn_decode(const uint16_t* q, int64_t q_sb, int64_t q_sh, int64_t q_st, int B, int Hq,
                        int Hkv, int T, int d, const void* k_pages, const void* v_pages,
